@@ -57,24 +57,29 @@ constexpr float kBs = 1024.0f;   // and B times this
 constexpr int kNormThreads = 256;
 constexpr int kNormMaxParts = 256;  // blocks per matrix in the norm's first pass
 
-// Three accumulators keep the sum of squares in range whatever G's scale:
-// values above 2^50 enter times 2^-80, those below 2^-50 times 2^80.
+// A sum of squares, sum * 4^back.  What one block or warp adds up is taken as it is
+// where that ends between 2^-90 and 2^118, else once more with every value times
+// 2^100 or 2^-100.  So each stays clear of both ends of the range, up to 256 of them
+// add up below 2^128, and no element is in another unit than its neighbours: G times
+// a power of two goes through the same roundings.
 struct Sq {
-    float big, mid, small;
+    float sum;
+    int back;  // -100, 0 or 100
 };
-__device__ __forceinline__ void sq_add(Sq &s, float v)
+__device__ __forceinline__ int back_of(float plain)  // 100 for a NaN too
 {
-    const float m = fabsf(v);
-    if (m > 0x1p50f)
-        s.big = fmaf(v * 0x1p-80f, v * 0x1p-80f, s.big);
-    else if (m < 0x1p-50f)
-        s.small = fmaf(v * 0x1p80f, v * 0x1p80f, s.small);
-    else
-        s.mid = fmaf(v, v, s.mid);
+    return plain <= 0x1p-90f ? -100 : (plain < 0x1p118f ? 0 : 100);
 }
-// A plain sum of squares that neither overflowed nor lost anything to
-// underflow: the three accumulators are for the others (and for zeros).
-__device__ __forceinline__ bool in_range(float sum) { return sum > 0x1p-60f && sum < 0x1p126f; }
+__device__ __forceinline__ float factor_of(int back) { return back > 0 ? 0x1p-100f : 0x1p100f; }
+// The sum in units of 4^back, back being at least its own or the sum zero.
+__device__ __forceinline__ float in_units(Sq s, int back)
+{
+    if (s.back == back)
+        return s.sum;
+    return back - s.back == 100 ? s.sum * 0x1p-100f * 0x1p-100f : 0.0f;
+}
+// The largest unit of those that hold anything.
+__device__ __forceinline__ int larger(int back, Sq s) { return s.sum != 0.0f && s.back > back ? s.back : back; }
 
 __device__ __forceinline__ float block_sum(float v, float *sm)
 {
@@ -96,23 +101,17 @@ struct Scale {
     int e;       // X_0 is stored as G * 2^e
     float unit;  // X_0 = unit * stored
 };
-// Norm = 2^k f with 1 <= f < 2 for each of the three ranges of the sum.
+// Norm = 2^k f with 1 <= f < 2, in units of 2^back.
 __device__ __forceinline__ Scale scale_of(Sq s)
 {
-    if (!(s.big + s.mid + s.small < INFINITY))
+    if (!(s.sum < INFINITY))
         return Scale{0, nanf("")};
-    int back = 0;
-    float sum = s.mid + s.small * 0x1p-80f * 0x1p-80f;
-    if (s.big > 0.0f)
-        back = 80, sum = s.big + s.mid * 0x1p-80f * 0x1p-80f;
-    else if (!(s.mid > 0.0f))
-        back = -80, sum = s.small;
-    if (sum == 0.0f)
+    if (s.sum == 0.0f)
         return Scale{0, 0.0f};
-    const float norm = sqrtf(sum);
+    const float norm = sqrtf(s.sum);
     const int k = ilogbf(norm);
     // stored norm: norm 2^back 2^e = f 2^14
-    return Scale{14 - k - back, 1.0f / ldexpf(norm, 14 - k)};
+    return Scale{14 - k - s.back, 1.0f / ldexpf(norm, 14 - k)};
 }
 
 // Eight neighbouring values, of which `count` are there; the others are zero.
@@ -184,16 +183,15 @@ __global__ void __launch_bounds__(kNormThreads)
     float plain = 0.0f;
     each([&](float v) { plain = fmaf(v, v, plain); });
     plain = block_sum(plain, sm);
-    if (in_range(plain)) {
-        if (threadIdx.x == 0)
-            part[(long long)blockIdx.y * parts + blockIdx.x] = Sq{0.0f, plain, 0.0f};
-        return;
+    const int back = back_of(plain);
+    if (back != 0) {
+        const float f = factor_of(back);
+        plain = 0.0f;
+        each([&](float v) { plain = fmaf(v * f, v * f, plain); });
+        plain = block_sum(plain, sm);
     }
-    Sq s{0.0f, 0.0f, 0.0f};
-    each([&](float v) { sq_add(s, v); });
-    const Sq t{block_sum(s.big, sm), block_sum(s.mid, sm), block_sum(s.small, sm)};
     if (threadIdx.x == 0)
-        part[(long long)blockIdx.y * parts + blockIdx.x] = t;
+        part[(long long)blockIdx.y * parts + blockIdx.x] = Sq{plain, back};
 }
 
 __device__ __forceinline__ void two_terms(float v, __half &hi, __half &lo)
@@ -212,10 +210,12 @@ __global__ void __launch_bounds__(kNormThreads)
     __shared__ float sm[kNormThreads / 32];
     __shared__ float tile[64][33];
     const long long b = blockIdx.z;
-    Sq s{0.0f, 0.0f, 0.0f};
+    Sq s{0.0f, -100};
     if ((int)threadIdx.x < parts)
         s = part[b * parts + threadIdx.x];
-    const Scale sc = scale_of(Sq{block_sum(s.big, sm), block_sum(s.mid, sm), block_sum(s.small, sm)});
+    const bool held = s.sum != 0.0f;
+    const int back = __syncthreads_or(held && s.back > 0) ? 100 : (__syncthreads_or(held && s.back == 0) ? 0 : -100);
+    const Scale sc = scale_of(Sq{block_sum(in_units(s, back), sm), back});
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
         unit[b] = sc.unit;
     // 2^e in two factors, each in range

@@ -198,33 +198,31 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
         each([&](float v) { plain = fmaf(v, v, plain); });
         for (int d = 16; d; d >>= 1)
             plain += __shfl_xor_sync(0xffffffffu, plain, d);
-        Sq s{0.0f, plain, 0.0f};
-        if (!in_range(plain)) {
-            s.mid = 0.0f;
-            each([&](float v) { sq_add(s, v); });
-            for (int d = 16; d; d >>= 1) {
-                s.big += __shfl_xor_sync(0xffffffffu, s.big, d);
-                s.mid += __shfl_xor_sync(0xffffffffu, s.mid, d);
-                s.small += __shfl_xor_sync(0xffffffffu, s.small, d);
-            }
+        const int back = back_of(plain);
+        if (back != 0) {
+            const float f = factor_of(back);
+            plain = 0.0f;
+            each([&](float v) { plain = fmaf(v * f, v * f, plain); });
+            for (int d = 16; d; d >>= 1)
+                plain += __shfl_xor_sync(0xffffffffu, plain, d);
         }
         if (lane == 0)
-            sm.warp[warp] = s;
+            sm.warp[warp] = Sq{plain, back};
     }
     __syncthreads();
     if (warp < stacked) {
-        Sq s{0.0f, 0.0f, 0.0f};
-        for (int w = 0; w < rows / kRows; ++w) {
-            const Sq t = sm.warp[warp * (rows / kRows) + w];
-            s.big += t.big, s.mid += t.mid, s.small += t.small;
-        }
+        const int count = rows / kRows;
+        const Sq *const at = sm.warp + warp * count;
+        const int back = __reduce_max_sync(0xffffffffu, lane < count ? larger(-100, at[lane]) : -100);
+        Sq s{0.0f, back};
+        for (int w = 0; w < count; ++w)
+            s.sum += in_units(at[w], back);
         if (lane < ranks) {
             const uint32_t to = smem_u32(&sm.part[rank][warp]);
             if (CL) {
                 const uint32_t far = at_rank(to, lane);
-                far_store(far, __float_as_uint(s.big));
-                far_store(far + 4, __float_as_uint(s.mid));
-                far_store(far + 8, __float_as_uint(s.small));
+                far_store(far, __float_as_uint(s.sum));
+                far_store(far + 4, (uint32_t)s.back);
             } else {
                 sm.part[0][warp] = s;
             }
@@ -237,11 +235,11 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
         __syncthreads();
     }
     if (threadIdx.x < stacked) {
-        Sq s{0.0f, 0.0f, 0.0f};
-        for (int r = 0; r < ranks; ++r) {
-            const Sq t = sm.part[r][threadIdx.x];
-            s.big += t.big, s.mid += t.mid, s.small += t.small;
-        }
+        Sq s{0.0f, -100};
+        for (int r = 0; r < ranks; ++r)
+            s.back = larger(s.back, sm.part[r][threadIdx.x]);
+        for (int r = 0; r < ranks; ++r)
+            s.sum += in_units(sm.part[r][threadIdx.x], s.back);
         Scale sc = scale_of(s);
         if (!(sc.unit < INFINITY)) {
             sc = Scale{0, 0.0f};

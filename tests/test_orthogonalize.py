@@ -298,3 +298,35 @@ def test_refusals_of_the_library():
     import torch
     if not torch.cuda.is_available():
         assert lib.bstq_orthogonalize(*good) == bstq.ERR_NODEVICE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,kind", [(1531, 777, "gradient"), (2048, 2048, "gradient"), (128, 128, "gradient"),
+                                      (128, 4096, "gradient"), (90, 600, "graded"), (700, 900, "graded")])
+def test_scale_does_not_matter_at_any_exponent(m, n, kind):
+    """Every power of two at which G's values stay normal: the sums of squares
+    that blocks, warps and clusters join must neither overflow nor change a
+    rounding.  "graded": rows of very different sizes, whose sums are taken in
+    different ranges."""
+    import torch
+    G = matrices(1, m, n, "float32", seed=5, kind="gradient")
+    if kind == "graded":
+        G = G * (2.0 ** -(5.0 * (torch.arange(m, device="cuda") % 8)))[:, None]
+    want = bstq.orthogonalize(G)
+    assert torch.isfinite(want).all()
+    if kind == "gradient":
+        check(want, G, "float32")
+    bad = [k for k in range(-60 if kind == "graded" else -100, 121)
+           if not torch.equal(bstq.orthogonalize(G * 2.0 ** k), want)]
+    assert not bad, bad
+
+
+@pytest.mark.gpu
+def test_norm_of_the_largest_and_smallest_values():
+    """All values at float32's ends, where no square and hardly a value fits."""
+    import torch
+    for size in ((1, 100, 130), (1, 300, 260)):
+        sign = torch.where(torch.randn(size, generator=torch.Generator().manual_seed(1)) > 0, 1.0, -1.0).cuda()
+        want = bstq.orthogonalize(sign)
+        for top in (3.0e38, 2.0 ** -149, 2.0 ** -140):
+            assert torch.allclose(bstq.orthogonalize(sign * top), want, rtol=0, atol=2e-6), top
