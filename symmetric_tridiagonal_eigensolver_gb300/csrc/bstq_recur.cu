@@ -73,11 +73,10 @@ __device__ __forceinline__ float rcp(float v)
 }
 constexpr float kLog2e = 1.44269504f;
 
-// 1 - exp(-z) for z >= 0 to two units in the last place: below 3/4 z times the
-// Chebyshev interpolant of (1 - exp(-z)) / z of degree 5 (off by 3.3e-8 at
-// most), above it one minus the exponential.
+// 1 - exp(-z) for 0 <= z < 3/4 to two units in the last place: z times the Chebyshev
+// interpolant of (1 - exp(-z)) / z of degree 5 (off by 3.3e-8 at most).
 template <int V>
-__device__ __forceinline__ Pk<V> one_minus_exp(Pk<V> z)
+__device__ __forceinline__ Pk<V> near_zero(Pk<V> z)
 {
     Pk<V> f = pk_all<V>(-0.0010119646f);
     f = fma_(f, z, pk_all<V>(0.0080331592f));
@@ -85,18 +84,49 @@ __device__ __forceinline__ Pk<V> one_minus_exp(Pk<V> z)
     f = fma_(f, z, pk_all<V>(0.1666469872f));
     f = fma_(f, z, pk_all<V>(-0.4999987483f));
     f = fma_(f, z, pk_all<V>(1.0f));
-    f = mul_(f, z);
+    return mul_(f, z);
+}
+template <int V>
+__device__ __forceinline__ Pk<V> exp_minus(Pk<V> z)
+{
     const Pk<V> y = mul_(z, pk_all<V>(-kLog2e));
-    float e[V], out[V];
+    float e[V];
 #pragma unroll
     for (int k = 0; k < V; ++k)
         e[k] = ex2(y.get(k));
-    const Pk<V> g = fma_(pk<V>(e), pk_all<V>(-1.0f), pk_all<V>(1.0f));
+    return pk<V>(e);
+}
+
+// 1 - exp(-z) for z >= 0: from 3/4 on one minus the exponential.
+template <int V>
+__device__ __forceinline__ Pk<V> one_minus_exp(Pk<V> z)
+{
+    const Pk<V> f = near_zero<V>(z), g = fma_(exp_minus<V>(z), pk_all<V>(-1.0f), pk_all<V>(1.0f));
+    float out[V];
 #pragma unroll
     for (int k = 0; k < V; ++k)
         out[k] = z.get(k) < 0.75f ? f.get(k) : g.get(k);
     return pk<V>(out);
 }
+
+// The gradients need a = exp(-z) and 1 - a each to its own last digits: a is a
+// factor of dr, drate and dh0 (1 - (1 - a) in floats is off by 2.6e-2 of a at z = 15
+// and zero at 18), 1 - a one of dx.  One number holds both: -(1 - a) for z < 3/4,
+// else a.  It is the smaller of the two (at most 0.53), the other is one minus it,
+// and the sign bit tells which.
+__device__ __forceinline__ bool is_loss(float n) { return __float_as_int(n) < 0; }
+__device__ __forceinline__ Pk<2> decay(Pk<2> z)
+{
+    const Pk<2> f = near_zero<2>(z), e = exp_minus<2>(z);
+    return Pk<2>::make(z.get(0) < 0.75f ? -f.get(0) : e.get(0), z.get(1) < 0.75f ? -f.get(1) : e.get(1));
+}
+// g where n is a loss, else zero: a g = n g + whole, (1 - a) g = (g - whole) - n g.
+__device__ __forceinline__ Pk<2> whole(Pk<2> n, Pk<2> g)
+{
+    return Pk<2>::make(is_loss(n.get(0)) ? g.get(0) : 0.0f, is_loss(n.get(1)) ? g.get(1) : 0.0f);
+}
+__device__ __forceinline__ float kept(float n, float g) { return fmaf(n, g, is_loss(n) ? g : 0.0f); }  // a g
+__device__ __forceinline__ Pk<2> kept(Pk<2> n, Pk<2> g) { return fma_(n, g, whole(n, g)); }
 
 // s = sigma(r): the exponential's overflow gives 0.
 template <int V>
@@ -162,7 +192,7 @@ struct RecurArgs {
     // each of `chains` = batch * cols tiles of channels; a block goes from one
     // tile to its next by step_rank ranks and step_chain chains
     int ranks, cols, chains, step_rank, step_chain, group;
-    unsigned long long *maps;  // (v, Q): [chain][rank][64], then of four tiles, [chain][rank / 4][64]
+    unsigned long long *maps;  // (v, Q or, for the gradients, the number that decay() gives): [chain][rank][64], then of four tiles, [chain][rank / 4][64]
     uint32_t *states;          // [chain][group][64]
     int *status;
 };
@@ -253,24 +283,46 @@ __device__ __forceinline__ void publish_state(uint32_t *p, float v)
     asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(marked(v)) : "memory");
 }
 
-// A map h -> h + (v - q h) of each of a lane's two channels.
+// A map h -> h + (v - q h) of each of a lane's two channels.  FINE (the gradients):
+// h -> a h + v with a = 1 - q to its own digits, passed on as decay()'s number.
+template <bool FINE>
 struct Map2 {
-    float q[2], v[2];
-    __device__ __forceinline__ void then(const float (&mq)[2], const float (&mv)[2])
+    float q[2] = {0.0f, 0.0f}, v[2] = {0.0f, 0.0f}, a[2] = {1.0f, 1.0f};
+    static __device__ __forceinline__ float none() { return FINE ? -0.0f : 0.0f; }
+    __device__ __forceinline__ float passed(int c) const { return !FINE ? q[c] : (q[c] < 0.5f ? -q[c] : a[c]); }
+    __device__ __forceinline__ float of(int c, float h) const
+    {
+        return FINE ? kept(passed(c), h) + v[c] : h + (v[c] - q[c] * h);
+    }
+    __device__ __forceinline__ void then(const float (&m)[2], const float (&mv)[2])
     {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            v[c] += mv[c] - mq[c] * v[c];
-            q[c] += mq[c] - mq[c] * q[c];
+            if (FINE) {
+                const bool loss = is_loss(m[c]);
+                const float mq = loss ? -m[c] : 1.0f - m[c];
+                v[c] = kept(m[c], v[c]) + mv[c];
+                q[c] += mq - mq * q[c];
+                a[c] *= loss ? 1.0f + m[c] : m[c];
+            } else {
+                v[c] += mv[c] - m[c] * v[c];
+                q[c] += m[c] - m[c] * q[c];
+            }
         }
+    }
+    __device__ __forceinline__ void then(const Map2 &next)
+    {
+        const float m[2] = {next.passed(0), next.passed(1)};
+        then(m, next.v);
     }
 };
 
 // Reads up to three published maps in a row (`n` of them) and joins them; false
 // while one is missing.
-__device__ __forceinline__ bool read_maps(const unsigned long long *at, int n, Map2 &m)
+template <bool FINE>
+__device__ __forceinline__ bool read_maps(const unsigned long long *at, int n, Map2<FINE> &m)
 {
-    m = Map2{{0.0f, 0.0f}, {0.0f, 0.0f}};
+    m = Map2<FINE>{};
     if (n <= 0)
         return true;
     unsigned long long w[3][2];
@@ -285,7 +337,7 @@ __device__ __forceinline__ bool read_maps(const unsigned long long *at, int n, M
         for (int c = 0; c < 2; ++c) {
             const uint32_t mark = (uint32_t)(w[i][c] >> 32);
             there = there && mark != kUnset;
-            q[c] = i < n ? __uint_as_float(mark) : 0.0f;
+            q[c] = i < n ? __uint_as_float(mark) : Map2<FINE>::none();
             v[c] = i < n ? __uint_as_float((uint32_t)w[i][c]) : 0.0f;
         }
         m.then(q, v);
@@ -298,7 +350,7 @@ __device__ __forceinline__ bool read_maps(const unsigned long long *at, int n, M
 // its four tiles, or the state after its group) and returns the state after the
 // tile.  `first` is the channels' first tile, `last` their last.  `between` runs
 // when every warp has its map.
-template <bool EARLY, int W, typename F>
+template <bool GRAD, int W, typename F>
 __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int slot, uint32_t phase, int chain_id, int rank,
                                       int first, int last, const float *start, const bool (&on)[2], F between,
                                       float (&enter)[2], float (&after)[2])
@@ -313,7 +365,8 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
     uint32_t *states = a.states + (long long)chain_id * groups * kChannels + 2 * lane;
     unsigned long long *singles = a.maps + at * kChannels + 2 * lane;
     unsigned long long *fours = a.maps + ((long long)a.chains * a.ranks + (long long)chain_id * ((a.ranks + 3) / 4)) * kChannels + 2 * lane;
-    Map2 own{{0.0f, 0.0f}, {0.0f, 0.0f}}, near = own;
+    constexpr bool EARLY = !GRAD;
+    Map2<GRAD> own, near;
     bool have_near = single == rank, entered = false, mine = false;
     const uint32_t ready = smem_u32(&sm.ready[slot]);
     auto leave = [&] {
@@ -326,13 +379,13 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
         if (rank >= last)
             return;
         if (rank - four < 3) {
-            publish_map(singles + (long long)rank * kChannels, own.q[0], own.v[0]);
-            publish_map(singles + (long long)rank * kChannels + 1, own.q[1], own.v[1]);
+            publish_map(singles + (long long)rank * kChannels, own.passed(0), own.v[0]);
+            publish_map(singles + (long long)rank * kChannels + 1, own.passed(1), own.v[1]);
         } else if (rank % a.group < a.group - 1) {
-            Map2 all = near;
-            all.then(own.q, own.v);
-            publish_map(fours + (long long)(rank / 4) * kChannels, all.q[0], all.v[0]);
-            publish_map(fours + (long long)(rank / 4) * kChannels + 1, all.q[1], all.v[1]);
+            Map2<GRAD> all = near;
+            all.then(own);
+            publish_map(fours + (long long)(rank / 4) * kChannels, all.passed(0), all.v[0]);
+            publish_map(fours + (long long)(rank / 4) * kChannels + 1, all.passed(1), all.v[1]);
         }
     };
     const bool maps = a.group > 1;
@@ -354,15 +407,13 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
                 enter[0] = on[0] ? start[0] : 0.0f;
                 enter[1] = on[1] ? start[1] : 0.0f;
             }
-            Map2 far{{0.0f, 0.0f}, {0.0f, 0.0f}};
+            Map2<GRAD> far;
             if (maps)
                 there = read_maps(fours + (long long)(from / 4) * kChannels, rank / 4 - from / 4, far) && there;
             if (__all_sync(0xffffffffu, there) && have_near) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    enter[c] += far.v[c] - far.q[c] * enter[c];
-                    enter[c] += near.v[c] - near.q[c] * enter[c];
-                }
+                for (int c = 0; c < 2; ++c)
+                    enter[c] = near.of(c, far.of(c, enter[c]));
                 entered = true;
                 if (EARLY || mine)
                     leave();
@@ -393,8 +444,8 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
             *(volatile int *)a.status = 1;
         }
     } while (__any_sync(0xffffffffu, *(volatile int *)&sm.stop == 0));
-    after[0] = enter[0] + (own.v[0] - own.q[0] * enter[0]);
-    after[1] = enter[1] + (own.v[1] - own.q[1] * enter[1]);
+    after[0] = own.of(0, enter[0]);
+    after[1] = own.of(1, enter[1]);
     if (rank < last && rank % a.group == a.group - 1) {
         publish_state(states + (long long)group * kChannels, after[0]);
         publish_state(states + (long long)group * kChannels + 1, after[1]);
@@ -445,7 +496,7 @@ struct LaneRun {
     T *tile;  // the stage, at this lane's channels
     const Place &p;
     int warp, lane;
-    Pk<2> q[L], s[GRAD ? L : 1];
+    Pk<2> q[L], s[GRAD ? L : 1];  // 1 - a; for the gradients decay()'s numbers, and the gates
 
     // the row of token t in the tile, and the token itself; for the gradients
     // t counts backwards
@@ -469,11 +520,13 @@ struct LaneRun {
             if (GRAD)
                 s[GRAD ? t : 0] = g;
             const Pk<2> zt = mul_(rate, g);
-            q[t] = one_minus_exp<2>(zt);
+            q[t] = GRAD ? decay(zt) : one_minus_exp<2>(zt);
             z = add_(z, zt);
             if (GRAD) {
                 v = add_(v, get2(at(3, t)));
-                v = fma_(neg_<2>(q[t]), v, v);
+                // as in whole(), by the comparison that decay() has made
+                const Pk<2> w = Pk<2>::make(zt.get(0) < 0.75f ? v.get(0) : 0.0f, zt.get(1) < 0.75f ? v.get(1) : 0.0f);
+                v = fma_(q[t], v, w);
             } else {
                 v = fma_(q[t], sub_<2>(get2(at(0, t)), v), v);
             }
@@ -517,8 +570,8 @@ struct LaneRun {
                 continue;
             }
             g = add_(g, get2(at(3, t)));
-            const Pk<2> gx = mul_(q[t], g);
-            g = fma_(neg_<2>(q[t]), g, g);
+            const Pk<2> w = whole(q[t], g), gx = sub_(sub_(g, w), mul_(q[t], g));
+            g = fma_(q[t], g, w);
             Pk<2> before = get2(at(2, t));
             if (t == L - 1 && token(t) == 0)
                 before = h0;
@@ -637,7 +690,7 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
                 const long long at = (long long)c.b * a.dim + c.j0 + 2 * lane;
                 float enter[2], after[2];
                 // the sums have one place: no warp gets to its next ones before they are read
-                chain<!GRAD, S::W>(a, sm, slot, phase, c.ch, c.rank, c.first, c.last, from ? from + at : nullptr, on, sums,
+                chain<GRAD, S::W>(a, sm, slot, phase, c.ch, c.rank, c.first, c.last, from ? from + at : nullptr, on, sums,
                              enter, after);
                 if (c.rank == c.last && to)
 #pragma unroll
@@ -670,7 +723,7 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
         for (int k = 0; k < 2; ++k) {
             const int j = p.j0 + 2 * lane + k;
             v[k] = j < a.dim ? a.rate[j] : 0.0f;
-            v[k] = v[k] < 0.0f ? 0.0f : v[k];
+            v[k] = v[k] <= 0.0f ? 0.0f : v[k];  // no zero with a sign
         }
         return pk<2>(v);
     };
@@ -712,7 +765,7 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
             LaneRun<T, GRAD, decltype(mask)::value, TMA> l{a, stage + 2 * lane, p, warp, lane, {}, {}};
             Pk<2> z, v;
             l.first(rate, z, v);
-            const Pk<2> qw = one_minus_exp<2>(z);
+            const Pk<2> qw = GRAD ? decay(z) : one_minus_exp<2>(z);
             put2(&sm.q[slot][warp][2 * lane], qw);
             put2(&sm.v[slot][warp][2 * lane], v);
             __syncwarp();
@@ -735,8 +788,10 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
             wait_for(sm, sm.ready[slot], phase, a.status);
             wait_for(sm, sm.entered[slot], phase, a.status);
             Pk<2> e = get2(&sm.enter[slot][2 * lane]);
-            for (int w = 0; w < warp; ++w)
-                e = add_(fma_(neg_<2>(get2(&sm.q[slot][w][2 * lane])), e, e), get2(&sm.v[slot][w][2 * lane]));
+            for (int w = 0; w < warp; ++w) {
+                const Pk<2> m = get2(&sm.q[slot][w][2 * lane]);
+                e = add_(GRAD ? kept(m, e) : fma_(neg_<2>(m), e, e), get2(&sm.v[slot][w][2 * lane]));
+            }
             if constexpr (GRAD) {
                 const Pk<2> sum = l.backward(e, rate, h0);
                 put2(&sm.sums[warp][2 * lane], sum);

@@ -563,3 +563,108 @@ def test_refusals_of_the_library():
     import torch
     if not torch.cuda.is_available():
         assert lib.bstq_recur(0, 2, 5, 8, p, p, p, p, p, p, p, None, p, None) == bstq.ERR_NODEVICE
+
+
+# --------------------------------------------------------------------------
+# Gradients where a gate or a decay saturates, element by element
+# --------------------------------------------------------------------------
+
+def own_size(x, r, rate, h, dh, dhT, h0):
+    """Gradients in 64 bits of sums without cancellation (dh, dhT, x - h >= 0) and
+    a bound on each element's relative error, counted in u = 2^-24.
+
+    The exponential of y = r log2 e has y's rounding, |r| u, and 4 u of its own;
+    the gate s, and 1 - s, (|r| + 8) u; z = lambda s (|r| + 9) u, so a = exp(-z)
+    is off by z (|r| + 9) u, by z u of its own y, and by 8 u.  A product of decays
+    has the sum of theirs.  A sum of positive terms is off by at most the mean of
+    what its terms are off by, weighted with them, and a rounding for each term."""
+    B, T, D = x.shape
+    s = 1 / (1 + np.exp(-r))
+    o = 1 / (1 + np.exp(r))  # 1 - s
+    lam = np.maximum(rate, 0)
+    z = lam * s
+    a, q = np.exp(-z), -np.expm1(-z)
+    gate = np.abs(r) + 8
+    off = z * (gate + 2) + 8
+    dx, dr, ds = np.zeros_like(x), np.zeros_like(x), np.zeros_like(x)
+    bx, br, bs = np.zeros_like(x), np.zeros_like(x), np.zeros_like(x)
+    g, bg = dhT.astype(np.float64).copy(), np.zeros((B, D))
+    for t in range(T - 1, -1, -1):
+        before = h[:, t - 1] if t else h0
+        new = g + dh[:, t]
+        bg = np.where(new > 0, g * bg / np.where(new > 0, new, 1), bg) + 3
+        g = new
+        dx[:, t] = q[:, t] * g
+        bx[:, t] = bg + gate[:, t] + 8
+        g = a[:, t] * g
+        bg = bg + off[:, t]
+        ds[:, t] = g * (x[:, t] - before) * s[:, t]
+        bs[:, t] = bg + gate[:, t] + 4
+        dr[:, t] = ds[:, t] * lam * o[:, t]
+        br[:, t] = bs[:, t] + gate[:, t] + 4
+    drate = ds.sum((0, 1))
+    brate = (ds * bs).sum((0, 1)) / np.maximum(drate, 1e-300) + 32 + 2 * (B * T) ** 0.5
+    return (dx, dr, drate, g), (bx, br, brate, bg)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T", [1, 6, 90, 400, 1500])
+@pytest.mark.parametrize("kind", ["large rates", "shut gates", "last token only"])
+def test_gradients_keep_their_digits_where_gates_saturate(kind, T, dtype):
+    """Rates of up to 30 and gates at up to |r| = 20: a = exp(-z), down to 1e-13, is a
+    factor of dr, drate and dh0, which have to be right relative to their own size."""
+    import torch
+    B, D = 2, 70
+    g = torch.Generator().manual_seed(T)
+
+    def positive(*shape):
+        return (torch.rand(*shape, generator=g) + 0.5).to(getattr(torch, dtype)).cuda()
+
+    x, h, dh = positive(B, T, D), -positive(B, T, D), positive(B, T, D)
+    lo, hi = {"large rates": (-3, 3), "open gates": (8, 20), "shut gates": (-20, -8), "last token only": (-3, 3)}[kind]
+    r = (lo + (hi - lo) * torch.rand(B, T, D, generator=g)).to(x.dtype).cuda()
+    top = {"large rates": 30.0, "open gates": 30.0, "shut gates": 1e4, "last token only": 6.0}[kind]
+    rate = torch.linspace(0.2 * top, top, D).cuda()
+    h0, dhT = -positive(B, D).float(), positive(B, D).float()
+    if kind == "last token only":
+        dh.zero_()
+    got = bstq.recur_grad(x, r, rate, h, dh, dhT=dhT, h0=h0)
+    want, bound = own_size(f64(x), f64(r), f64(rate), f64(h), f64(dh), f64(dhT), f64(h0))
+    for name, v, w, b, kind_of in zip(("dx", "dr", "drate", "dh0"), got, want, bound, (dtype, dtype, "float32", "float32")):
+        seen = w > 1e-30  # what 32 bits hold with room for the factors on the way
+        err = np.abs(f64(v) - w)[seen] / w[seen]
+        lim = b[seen] * U + HALF[kind_of]
+        assert (err <= lim).all(), (name, (err / lim).max())
+
+
+@pytest.mark.gpu
+def test_gradients_of_saturated_gates_against_differences():
+    """The loss sum(h dh) of the 64-bit recurrence, its slope along rate and r by
+    central differences with steps relative to what they change."""
+    import torch
+    B, T, D = 1, 12, 8
+    make, g = problem(B, T, D, "float32", seed=3)
+    x, dh = make(B, T, D), make(B, T, D)
+    r = make(B, T, D, shift=12.0)
+    rate = torch.linspace(9.0, 16.0, D).cuda()
+    h, _ = bstq.recur(x, r, rate)
+    _, dr, drate, _ = bstq.recur_grad(x, r, rate, h, dh)
+    base = [f64(x), f64(r), f64(rate)]
+
+    def loss(p, j):  # of channel j, less what does not depend on rate and r: h_t = x_t + a_t (h_{t-1} - x_t)
+        xx, rr, lam = p[0][0, :, j], p[1][0, :, j], p[2][j]
+        last, out = 0.0, 0.0
+        for t in range(T):
+            rest = np.exp(-lam / (1 + np.exp(-rr[t]))) * (last - xx[t])
+            out += rest * f64(dh)[0, t, j]
+            last = xx[t] + rest
+        return out
+
+    for j in range(D):
+        up, down = [v.copy() for v in base], [v.copy() for v in base]
+        up[2][j] += 1e-4
+        down[2][j] -= 1e-4
+        slope = (loss(up, j) - loss(down, j)) / 2e-4
+        # h enters as stored, rounded to 2^-24 of its size, which 1e-6 covers
+        assert abs(float(drate[j]) - slope) <= 1e-4 * abs(slope) + 1e-6 * np.exp(-base[2][j]) * T
