@@ -128,21 +128,28 @@ __device__ __forceinline__ Pk<2> whole(Pk<2> n, Pk<2> g)
 __device__ __forceinline__ float kept(float n, float g) { return fmaf(n, g, is_loss(n) ? g : 0.0f); }  // a g
 __device__ __forceinline__ Pk<2> kept(Pk<2> n, Pk<2> g) { return fma_(n, g, whole(n, g)); }
 
-// s = sigma(r): the exponential's overflow gives 0.
+// s = sigma(r) from e = exp(-r): where that overflows, 0.
 template <int V>
-__device__ __forceinline__ Pk<V> sigma(Pk<V> r)
+__device__ __forceinline__ Pk<V> sigma_of(Pk<V> e)
 {
-    const Pk<V> y = mul_(r, pk_all<V>(-kLog2e));
-    float e[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-        e[k] = ex2(y.get(k));
-    const Pk<V> d = add_(pk<V>(e), pk_all<V>(1.0f));
+    const Pk<V> d = add_(e, pk_all<V>(1.0f));
     float s[V];
 #pragma unroll
     for (int k = 0; k < V; ++k)
         s[k] = rcp(d.get(k));
     return pk<V>(s);
+}
+template <int V>
+__device__ __forceinline__ Pk<V> sigma(Pk<V> r)
+{
+    return sigma_of<V>(exp_minus<V>(r));
+}
+// 1 - s = e s to its own digits: 1 - s from a rounded s is off by 9e-3 at r = 12 and
+// zero at 17.  Where e overflows and s is zero their product is no number, and 1 - s one.
+__device__ __forceinline__ Pk<2> one_minus_sigma(Pk<2> s, Pk<2> e)
+{
+    const Pk<2> o = mul_(e, s);
+    return Pk<2>::make(fminf(o.get(0), 1.0f), fminf(o.get(1), 1.0f));
 }
 
 // A pair of neighbouring values in memory.
@@ -496,7 +503,7 @@ struct LaneRun {
     T *tile;  // the stage, at this lane's channels
     const Place &p;
     int warp, lane;
-    Pk<2> q[L], s[GRAD ? L : 1];  // 1 - a; for the gradients decay()'s numbers, and the gates
+    Pk<2> q[L], e[GRAD ? L : 1];  // 1 - a; for the gradients decay()'s numbers, and exp(-r)
 
     // the row of token t in the tile, and the token itself; for the gradients
     // t counts backwards
@@ -516,10 +523,9 @@ struct LaneRun {
                 q[t] = pk_all<2>(0.0f);
                 continue;
             }
-            const Pk<2> g = sigma<2>(get2(at(1, t)));
+            const Pk<2> er = exp_minus<2>(get2(at(1, t))), zt = mul_(rate, sigma_of<2>(er));
             if (GRAD)
-                s[GRAD ? t : 0] = g;
-            const Pk<2> zt = mul_(rate, g);
+                e[GRAD ? t : 0] = er;
             q[t] = GRAD ? decay(zt) : one_minus_exp<2>(zt);
             z = add_(z, zt);
             if (GRAD) {
@@ -576,10 +582,12 @@ struct LaneRun {
             if (t == L - 1 && token(t) == 0)
                 before = h0;
             const Pk<2> dz = mul_(g, sub_<2>(get2(at(0, t)), before));
-            const Pk<2> ds = mul_(dz, s[GRAD ? t : 0]);  // summed: drate; times lambda (1 - s): dr
+            // the gate once more: its registers would not fit beside e
+            const Pk<2> er = e[GRAD ? t : 0], s = sigma_of<2>(er);
+            const Pk<2> ds = mul_(dz, s);  // summed: drate; times lambda (1 - s): dr
             sum = add_(sum, ds);
             out(0, t, gx);
-            out(1, t, mul_(mul_(ds, rate), sub_<2>(pk_all<2>(1.0f), s[GRAD ? t : 0])));
+            out(1, t, mul_(mul_(ds, rate), one_minus_sigma(s, er)));
         }
         return sum;
     }

@@ -610,10 +610,11 @@ def own_size(x, r, rate, h, dh, dhT, h0):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("T", [1, 6, 90, 400, 1500])
-@pytest.mark.parametrize("kind", ["large rates", "shut gates", "last token only"])
+@pytest.mark.parametrize("kind", ["large rates", "open gates", "shut gates", "last token only"])
 def test_gradients_keep_their_digits_where_gates_saturate(kind, T, dtype):
-    """Rates of up to 30 and gates at up to |r| = 20: a = exp(-z), down to 1e-13, is a
-    factor of dr, drate and dh0, which have to be right relative to their own size."""
+    """Rates of 8 to 30 and gates at up to |r| = 20: a = exp(-z) down to 1e-13 and
+    1 - s down to 2e-9 are factors of dr, drate and dh0, which have to be right
+    relative to their own size."""
     import torch
     B, D = 2, 70
     g = torch.Generator().manual_seed(T)
