@@ -1090,7 +1090,7 @@ extern "C" int bstq_orthogonalize(bstq_dtype dtype, int64_t batch, int64_t m, in
     for (int i = 0; i < 4; ++i)
         if (st[i] < 0 || st[i] > (1LL << 42))
             return -7;
-    if ((m > 1 && st[3] < n) || (batch > 1 && st[2] < n))
+    if (!rows_apart(n, m, st[3], batch, st[2]))
         return -7;
     if (steps < 1 || steps > kMaxSteps)
         return -8;

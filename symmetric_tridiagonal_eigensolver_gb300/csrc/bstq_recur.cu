@@ -977,11 +977,7 @@ bool strides_ok(const int64_t *strides, int count)
     return true;
 }
 
-// An output's elements are apart: rows of dim values do not overlap.
-bool apart(const Seq &s, int64_t batch, int64_t time, int64_t dim)
-{
-    return time == 0 || ((batch <= 1 || s.sb >= dim) && (time <= 1 || s.st >= dim));
-}
+bool apart(const Seq &s, int64_t batch, int64_t time, int64_t dim) { return rows_apart(dim, time, s.st, batch, s.sb); }
 
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 

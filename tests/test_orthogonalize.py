@@ -330,3 +330,20 @@ def test_norm_of_the_largest_and_smallest_values():
         want = bstq.orthogonalize(sign)
         for top in (3.0e38, 2.0 ** -149, 2.0 ** -140):
             assert torch.allclose(bstq.orthogonalize(sign * top), want, rtol=0, atol=2e-6), top
+
+
+def test_results_whose_rows_overlap_are_refused():
+    import os
+    if not os.path.exists(bstq.LIB_PATH):
+        from symmetric_tridiagonal_eigensolver_gb300 import build
+        build.build()
+    lib = bstq.load()
+    buf = (ctypes.c_char * 4096)()
+    p = ctypes.c_void_p(ctypes.addressof(buf) + (-ctypes.addressof(buf)) % 256)
+    for xb, xr in ((6, 6), (12, 6), (23, 6), (8, 13), (6, 17)):
+        assert lib.bstq_orthogonalize(0, 3, 4, 6, p, p, (ctypes.c_int64 * 4)(24, 6, xb, xr), 5, None, p, None) == -7, (xb, xr)
+    import torch
+    if not torch.cuda.is_available():
+        for xb, xr in ((24, 6), (25, 6), (6, 18), (30, 7), (40, 6)):
+            assert lib.bstq_orthogonalize(0, 3, 4, 6, p, p, (ctypes.c_int64 * 4)(24, 6, xb, xr), 5, None, p,
+                                          None) == bstq.ERR_NODEVICE, (xb, xr)

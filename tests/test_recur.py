@@ -669,3 +669,40 @@ def test_gradients_of_saturated_gates_against_differences():
         slope = (loss(up, j) - loss(down, j)) / 2e-4
         # h enters as stored, rounded to 2^-24 of its size, which 1e-6 covers
         assert abs(float(drate[j]) - slope) <= 1e-4 * abs(slope) + 1e-6 * np.exp(-base[2][j]) * T
+
+
+def test_outputs_whose_rows_overlap_are_refused():
+    """An output's two strides have to keep all its rows apart, not only the
+    neighbours along one axis: rows that two tiles write would race."""
+    lib = _lib()
+    import torch
+    buf = (ctypes.c_char * 4096)()
+    p = ctypes.c_void_p(ctypes.addressof(buf) + (-ctypes.addressof(buf)) % 256)
+
+    def overlap(rows, n0, s0, n1, s1):
+        at = sorted(i * s0 + j * s1 for i in range(n0) for j in range(n1))
+        return any(b - a < rows for a, b in zip(at, at[1:]))
+
+    rng = np.random.default_rng(0)
+    layouts = [(2, 5, 8, 8, 8), (2, 5, 16, 8, 8), (2, 5, 40, 8, 8), (2, 5, 39, 8, 8), (2, 5, 8, 16, 8), (2, 5, 8, 15, 8),
+               (2, 3, 6, 4, 2), (3, 2, 4, 6, 2), (2, 3, 7, 4, 2), (1, 5, 0, 8, 8), (2, 1, 8, 0, 8), (4, 4, 30, 10, 8)]
+    layouts += [tuple(int(v) for v in rng.integers(1, [6, 6, 40, 40, 9])) for _ in range(300)]
+    some = 0
+    for batch, time, sb, st, dim in layouts:
+        bad = overlap(dim, batch, sb, time, st)
+        some += not bad
+        if not bad and torch.cuda.is_available():
+            continue  # these pointers are no device memory
+        want = -12 if bad else bstq.ERR_NODEVICE
+        dense = [time * dim, dim]
+        assert lib.bstq_recur(0, batch, time, dim, p, p, p, None, None, p, None,
+                              (ctypes.c_int64 * 6)(*dense, *dense, sb, st), p, None) == want, (batch, time, sb, st, dim)
+        for k in (4, 5):
+            strides = dense * 6
+            strides[2 * k:2 * k + 2] = sb, st
+            assert lib.bstq_recur_grad(0, batch, time, dim, p, p, p, p, p, None, None, None, p, p, p, None,
+                                       (ctypes.c_int64 * 12)(*strides), p, None) == (-17 if bad else want)
+    assert 20 < some < len(layouts) - 20
+    far = 1 << 42  # no overflow on the way
+    wide = (ctypes.c_int64 * 6)(40, 8, 40, 8, far, far - 3)
+    assert lib.bstq_recur(0, 1 << 9, 1 << 9, 8, p, p, p, None, None, p, None, wide, p, None) == -12
