@@ -493,8 +493,8 @@ def _workspace(q, where, work, x, *shape):
         raise BstqError(-10, f"bstq_{where}_work_size")
     if work is None:
         return q.empty((nbytes,), dtype=q.u8, device=x.device)
-    if work.get_device() != x.get_device() or work.numel() * work.element_size() < nbytes:
-        raise ValueError(f"bstq.{where}: work needs {nbytes} bytes on {x.device}")
+    if work.get_device() != x.get_device() or work.numel() * work.element_size() < nbytes or not work.is_contiguous():
+        raise ValueError(f"bstq.{where}: work needs {nbytes} contiguous bytes on {x.device}")
     return work
 
 

@@ -706,3 +706,18 @@ def test_outputs_whose_rows_overlap_are_refused():
     far = 1 << 42  # no overflow on the way
     wide = (ctypes.c_int64 * 6)(40, 8, 40, 8, far, far - 3)
     assert lib.bstq_recur(0, 1 << 9, 1 << 9, 8, p, p, p, None, None, p, None, wide, p, None) == -12
+
+
+@pytest.mark.gpu
+def test_a_workspace_with_gaps_or_repeats_is_refused():
+    """An expanded tensor counts more elements than its memory has."""
+    import torch
+    x = torch.zeros(2, 900, 64, device="cuda")
+    rate = torch.ones(64, device="cuda")
+    G = torch.zeros(200, 300, device="cuda")
+    one = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    for work in (one.expand(1 << 28), torch.zeros(1 << 28, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        for call in (lambda: bstq.recur(x, x, rate, work=work), lambda: bstq.recur_grad(x, x, rate, x, x, work=work),
+                     lambda: bstq.orthogonalize(G, work=work)):
+            with pytest.raises(ValueError, match="contiguous"):
+                call()
