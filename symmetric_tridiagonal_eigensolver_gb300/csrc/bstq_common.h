@@ -25,6 +25,8 @@ int cuda_fail(cudaError_t err, const char *what);
 // apart in each of n1 groups that are s1 apart.
 inline bool rows_apart(int64_t row, int64_t n0, int64_t s0, int64_t n1, int64_t s1)
 {
+    if (n0 == 0 || n1 == 0)
+        return true;
     if (n0 < n1) {
         const int64_t n = n0, s = s0;
         n0 = n1, s0 = s1, n1 = n, s1 = s;

@@ -721,3 +721,17 @@ def test_a_workspace_with_gaps_or_repeats_is_refused():
                      lambda: bstq.orthogonalize(G, work=work)):
             with pytest.raises(ValueError, match="contiguous"):
                 call()
+
+
+def test_no_token_is_no_overlap():
+    """A call without tokens has no rows, whatever its strides."""
+    lib = _lib()
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are no device memory")
+    buf = (ctypes.c_char * 4096)()
+    p = ctypes.c_void_p(ctypes.addressof(buf) + (-ctypes.addressof(buf)) % 256)
+    for strides in (None, (ctypes.c_int64 * 6)(*([0, 0] * 3))):
+        assert lib.bstq_recur(0, 2, 0, 8, None, None, p, None, None, None, p, strides, p, None) == bstq.ERR_NODEVICE
+    assert lib.bstq_recur_grad(0, 2, 0, 8, None, None, p, None, None, None, None, None, None, None, p, p, None, p,
+                               None) == bstq.ERR_NODEVICE
