@@ -199,8 +199,10 @@ struct RecurArgs {
     // each of `chains` = batch * cols tiles of channels; a block goes from one
     // tile to its next by step_rank ranks and step_chain chains
     int ranks, cols, chains, step_rank, step_chain, group;
-    unsigned long long *maps;  // (v, Q or, for the gradients, the number that decay() gives): [chain][rank][64], then of four tiles, [chain][rank / 4][64]
-    uint32_t *states;          // [chain][group][64]
+    // (v, Q or, for the gradients, decay()'s number): [chain][rank][64], then of four
+    // tiles, [chain][rank / 4][64]
+    unsigned long long *maps;
+    unsigned long long *states;  // two channels to a word, [chain][group][32]
     int *status;
 };
 
@@ -285,9 +287,12 @@ __device__ __forceinline__ void publish_map(unsigned long long *p, float q, floa
     const unsigned long long bits = ((unsigned long long)marked(q) << 32) | __float_as_uint(v);
     asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(bits) : "memory");
 }
-__device__ __forceinline__ void publish_state(uint32_t *p, float v)
+// The states of a lane's two channels, written and read as one word: accesses of
+// different sizes to one place are not ordered by the memory model.
+__device__ __forceinline__ void publish_states(unsigned long long *p, float a, float b)
 {
-    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(marked(v)) : "memory");
+    const unsigned long long bits = ((unsigned long long)marked(b) << 32) | marked(a);
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(bits) : "memory");
 }
 
 // A map h -> h + (v - q h) of each of a lane's two channels.  FINE (the gradients):
@@ -369,7 +374,7 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
     const int single = four > from ? four : from;
     const bool grouped = from > first;
     const long long at = (long long)chain_id * a.ranks;
-    uint32_t *states = a.states + (long long)chain_id * groups * kChannels + 2 * lane;
+    unsigned long long *states = a.states + (long long)chain_id * groups * (kChannels / 2) + lane;
     unsigned long long *singles = a.maps + at * kChannels + 2 * lane;
     unsigned long long *fours = a.maps + ((long long)a.chains * a.ranks + (long long)chain_id * ((a.ranks + 3) / 4)) * kChannels + 2 * lane;
     constexpr bool EARLY = !GRAD;
@@ -407,7 +412,7 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
             bool there = true;
             enter[0] = enter[1] = 0.0f;
             if (grouped) {
-                unsigned long long s = load_mark((const unsigned long long *)(states + (long long)(group - 1) * kChannels));
+                const unsigned long long s = load_mark(states + (long long)(group - 1) * (kChannels / 2));
                 there = (uint32_t)s != kUnset && (uint32_t)(s >> 32) != kUnset;
                 enter[0] = __uint_as_float((uint32_t)s), enter[1] = __uint_as_float((uint32_t)(s >> 32));
             } else if (start) {
@@ -453,10 +458,8 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
     } while (__any_sync(0xffffffffu, *(volatile int *)&sm.stop == 0));
     after[0] = own.of(0, enter[0]);
     after[1] = own.of(1, enter[1]);
-    if (rank < last && rank % a.group == a.group - 1) {
-        publish_state(states + (long long)group * kChannels, after[0]);
-        publish_state(states + (long long)group * kChannels + 1, after[1]);
-    }
+    if (rank < last && rank % a.group == a.group - 1)
+        publish_states(states + (long long)group * (kChannels / 2), after[0], after[1]);
 }
 
 __device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool in)
@@ -1061,7 +1064,7 @@ cudaError_t run_tiles(bstq_dtype dtype, RecurArgs a, const RecurPlan &p, char *w
     // groups of one have no maps
     const size_t maps_bytes = a.group == 1 ? 0 : 8 * size_t(p.chains) * (p.ranks + (p.ranks + 3) / 4) * kChannels;
     const size_t states_bytes = 4 * size_t(p.chains) * ((p.ranks + a.group - 1) / a.group) * kChannels;
-    a.states = (uint32_t *)(work + p.maps + maps_bytes);
+    a.states = (unsigned long long *)(work + p.maps + maps_bytes);
     a.step_rank = (int)(grid / a.chains), a.step_chain = (int)(grid % a.chains);
     if (a.ranks == 1) {  // no tile waits for another
         kernel<<<grid, S::THREADS, tile_smem<T, GRAD>(), st>>>(a, maps);
