@@ -1003,6 +1003,34 @@ RecurPlan recur_plan(bstq_dtype dtype, int64_t batch, int64_t time, int64_t dim,
     return p;
 }
 
+// The SMs that the stream's context may use: a green context has a part of the
+// device's, and blocks that wait for each other have to fit there.
+int sms_of(cudaStream_t st, int device)
+{
+    typedef CUresult (*GetCtx)(CUstream, CUcontext *, CUgreenCtx *);
+    typedef CUresult (*OfCtx)(CUcontext, CUdevResource *, CUdevResourceType);
+    typedef CUresult (*OfGreen)(CUgreenCtx, CUdevResource *, CUdevResourceType);
+    static const auto entry = [](const char *name) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult got;
+        if (cudaGetDriverEntryPointByVersion(name, &f, 12050, cudaEnableDefault, &got) != cudaSuccess ||
+            got != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return f;
+    };
+    static const GetCtx get = (GetCtx)entry("cuStreamGetCtx");
+    static const OfCtx of_ctx = (OfCtx)entry("cuCtxGetDevResource");
+    static const OfGreen of_green = (OfGreen)entry("cuGreenCtxGetDevResource");
+    CUcontext ctx = nullptr;
+    CUgreenCtx green = nullptr;
+    CUdevResource r{};
+    if (!get || !of_ctx || !of_green || get(st, &ctx, &green) != CUDA_SUCCESS ||
+        (green ? of_green(green, &r, CU_DEV_RESOURCE_TYPE_SM) : of_ctx(ctx, &r, CU_DEV_RESOURCE_TYPE_SM)) != CUDA_SUCCESS)
+        return device;
+    const int sms = (int)r.sm.smCount;
+    return sms > 0 && sms < device ? sms : device;
+}
+
 // Map of a batch x time x dim tensor in boxes of 64 channels by `rows` tokens.
 // False where its rows do not start on 16 bytes: those go by ordinary loads.
 bool tile_map(CUtensorMap *map, bstq_dtype dtype, const void *at, const Seq &s, const RecurArgs &a, int rows)
@@ -1058,7 +1086,7 @@ cudaError_t run_tiles(bstq_dtype dtype, RecurArgs a, const RecurPlan &p, char *w
         if (dev < 64)
             blocks[tma][dev].store(per_sm, std::memory_order_relaxed);
     }
-    const long long tiles = p.ranks * p.chains, room = (long long)per_sm * sms;
+    const long long tiles = p.ranks * p.chains, room = (long long)per_sm * (p.ranks > 1 ? sms_of(st, sms) : sms);
     const unsigned grid = (unsigned)(tiles < room ? tiles : room);
     a.group = a.chains >= (long long)grid ? 1 : kMaxGroup;
     // groups of one have no maps

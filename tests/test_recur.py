@@ -735,3 +735,62 @@ def test_no_token_is_no_overlap():
         assert lib.bstq_recur(0, 2, 0, 8, None, None, p, None, None, None, p, strides, p, None) == bstq.ERR_NODEVICE
     assert lib.bstq_recur_grad(0, 2, 0, 8, None, None, p, None, None, None, None, None, None, None, p, p, None, p,
                                None) == bstq.ERR_NODEVICE
+
+
+# --------------------------------------------------------------------------
+# A context with a part of the device's SMs
+# --------------------------------------------------------------------------
+
+class _Resource(ctypes.Structure):  # CUdevResource of an SM resource
+    _fields_ = [("type", ctypes.c_int), ("padding", ctypes.c_ubyte * 92), ("sms", ctypes.c_uint),
+                ("rest", ctypes.c_ubyte * 44)]
+
+
+_green = []  # streams that tensors have been used on live as long as the process
+
+
+def stream_on_a_part(sms):
+    """A stream of a green context with some `sms` SMs; skips where the driver makes
+    none."""
+    import torch
+    if not _green:
+        cu = ctypes.CDLL("libcuda.so.1")
+        whole, part, rest = _Resource(), _Resource(), _Resource()
+        count, desc, ctx, handle = ctypes.c_uint(1), ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_void_p()
+        ref = ctypes.byref
+        torch.zeros(1, device="cuda")  # the primary context
+        for call, args in ((cu.cuDeviceGetDevResource, (0, ref(whole), 1)),
+                           (cu.cuDevSmResourceSplitByCount, (ref(part), ref(count), ref(whole), ref(rest), 0, sms)),
+                           (cu.cuDevResourceGenerateDesc, (ref(desc), ref(part), 1)),
+                           (cu.cuGreenCtxCreate, (ref(ctx), desc, 0, 1)),
+                           (cu.cuGreenCtxStreamCreate, (ref(handle), ctx, 1, 0))):
+            if call(*args) != 0:
+                pytest.skip("no green contexts here")
+        assert sms <= part.sms < whole.sms
+        _green.extend((ctx, torch.cuda.ExternalStream(handle.value)))
+    return _green[1]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("B,T,D", [(1, 9000, 64), (2, 3000, 1024)])
+def test_a_context_with_a_part_of_the_sms(B, T, D, dtype):
+    """Tiles wait for each other, so the grid has to fit the stream's own SMs."""
+    import torch
+    make, g = problem(B, T, D, dtype, seed=4)
+    x, r, dh = make(B, T, D), make(B, T, D), make(B, T, D)
+    rate = torch.from_numpy(chain_rates(D)).cuda()
+    want = bstq.recur(x, r, rate)
+    grads = bstq.recur_grad(x, r, rate, want[0], dh)
+    torch.cuda.synchronize()
+    stream = stream_on_a_part(16)
+    got = bstq.recur(x, r, rate, stream=stream)
+    mine = bstq.recur_grad(x, r, rate, want[0], dh, stream=stream)
+    stream.synchronize()
+    # the same tiles joined in other groups: roundings of the states, and of the type
+    m = max(float(x.abs().max()), 1.0)
+    near(got[0], f64(want[0]), (64 + 16 * T ** 0.5) * U * m, dtype)
+    near(got[1], f64(want[1]), (64 + 16 * T ** 0.5) * U * m, "float32")
+    for u, v, kind in zip(mine, grads, (dtype, dtype, "float32", "float32")):
+        top = float(v.abs().max())
+        near(u, f64(v), (64 + 16 * (B * T) ** 0.5) * U * 4 * top, kind)
