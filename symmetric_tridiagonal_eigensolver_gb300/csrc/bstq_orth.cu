@@ -57,10 +57,10 @@ constexpr float kBs = 1024.0f;   // and B times this
 constexpr int kNormThreads = 256;
 constexpr int kNormMaxParts = 256;  // blocks per matrix in the norm's first pass
 
-// A sum of squares, sum * 4^back.  What one block or warp adds up is taken as it is
-// where that ends between 2^-90 and 2^118, else once more with every value times
-// 2^100 or 2^-100.  So each stays clear of both ends of the range, up to 256 of them
-// add up below 2^128, and no element is in another unit than its neighbours: G times
+// A sum of squares, sum * 4^back.  It is taken as it is where that ends between 2^-90
+// and 2^118, else once more with every value times 2^100 or 2^-100: for a whole matrix
+// in the small kernel, for what one block adds up here, of which up to 256 come
+// together below 2^128.  No element is in another unit than its neighbours, so G times
 // a power of two goes through the same roundings.
 struct Sq {
     float sum;
@@ -78,8 +78,6 @@ __device__ __forceinline__ float in_units(Sq s, int back)
         return s.sum;
     return back - s.back == 100 ? s.sum * 0x1p-100f * 0x1p-100f : 0.0f;
 }
-// The largest unit of those that hold anything.
-__device__ __forceinline__ int larger(int back, Sq s) { return s.sum != 0.0f && s.back > back ? s.back : back; }
 
 __device__ __forceinline__ float block_sum(float v, float *sm)
 {

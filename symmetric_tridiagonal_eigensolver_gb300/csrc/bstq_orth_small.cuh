@@ -61,8 +61,8 @@ struct SmallShape {
 };
 
 struct SmallShared {
-    Sq warp[16];
-    Sq part[16][8];  // [rank][matrix]
+    float warp[16], part[16][8];  // [rank][matrix]
+    Sq sum[8];
     Scale scale[8];
     int bad[8];
     uint64_t done;
@@ -179,68 +179,64 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
         read8(a.tall ? mat + (c0 + c) * a.gr + i : mat + i * a.gr + c0 + c, count, a.vector, v);
     };
 
-    // ---- the norms
-    {
-        auto each = [&](auto add) {
-            for (int n0 = 0; n0 < pieces; n0 += kFlight) {
-                float v[kFlight][8];
+    // ---- the norms: sums of squares, once more in another unit where a matrix's whole
+    // sum shows that 32 bits do not hold it
+    int back = 0;  // of this warp's matrix
+    for (bool again = false;; again = true) {
+        const float f = back ? factor_of(back) : 1.0f;
+        float sum = 0.0f;
+        for (int n0 = 0; n0 < pieces; n0 += kFlight) {
+            float v[kFlight][8];
 #pragma unroll
-                for (int n = 0; n < kFlight; ++n)
-                    fetch(n0 + n, v[n]);
+            for (int n = 0; n < kFlight; ++n)
+                fetch(n0 + n, v[n]);
 #pragma unroll
-                for (int n = 0; n < kFlight; ++n)
+            for (int n = 0; n < kFlight; ++n)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        add(v[n][k]);
-            }
-        };
-        float plain = 0.0f;
-        each([&](float v) { plain = fmaf(v, v, plain); });
+                for (int k = 0; k < 8; ++k)
+                    sum = fmaf(v[n][k] * f, v[n][k] * f, sum);
+        }
         for (int d = 16; d; d >>= 1)
-            plain += __shfl_xor_sync(0xffffffffu, plain, d);
-        const int back = back_of(plain);
-        if (back != 0) {
-            const float f = factor_of(back);
-            plain = 0.0f;
-            each([&](float v) { plain = fmaf(v * f, v * f, plain); });
-            for (int d = 16; d; d >>= 1)
-                plain += __shfl_xor_sync(0xffffffffu, plain, d);
-        }
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (lane == 0)
-            sm.warp[warp] = Sq{plain, back};
-    }
-    __syncthreads();
-    if (warp < stacked) {
-        const int count = rows / kRows;
-        const Sq *const at = sm.warp + warp * count;
-        const int back = __reduce_max_sync(0xffffffffu, lane < count ? larger(-100, at[lane]) : -100);
-        Sq s{0.0f, back};
-        for (int w = 0; w < count; ++w)
-            s.sum += in_units(at[w], back);
-        if (lane < ranks) {
-            const uint32_t to = smem_u32(&sm.part[rank][warp]);
-            if (CL) {
-                const uint32_t far = at_rank(to, lane);
-                far_store(far, __float_as_uint(s.sum));
-                far_store(far + 4, (uint32_t)s.back);
-            } else {
-                sm.part[0][warp] = s;
+            sm.warp[warp] = sum;
+        __syncthreads();
+        if (warp < stacked) {
+            float s = 0.0f;
+            for (int w = 0; w < rows / kRows; ++w)
+                s += sm.warp[warp * (rows / kRows) + w];
+            if (lane < ranks) {
+                if (CL)
+                    far_store(at_rank(smem_u32(&sm.part[rank][warp]), lane), __float_as_uint(s));
+                else
+                    sm.part[0][warp] = s;
             }
         }
-    }
-    if (CL) {
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
+        if (CL) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            __syncthreads();
+        }
+        if (threadIdx.x < stacked) {
+            float s = 0.0f;
+            for (int r = 0; r < ranks; ++r)
+                s += sm.part[r][threadIdx.x];
+            sm.sum[threadIdx.x].sum = s;
+            if (!again)
+                sm.sum[threadIdx.x].back = b0 + threadIdx.x < a.batch ? back_of(s) : 0;
+        }
+        // the same in every block of a cluster, which add the same sums
+        if (!__syncthreads_or(!again && threadIdx.x < stacked && sm.sum[threadIdx.x & 7].back != 0))
+            break;
+        back = sm.sum[mine].back;
+        if (CL) {  // the parts have been read
+            cluster_arrive();
+            cluster_wait();
+        }
     }
     if (threadIdx.x < stacked) {
-        Sq s{0.0f, -100};
-        for (int r = 0; r < ranks; ++r)
-            s.back = larger(s.back, sm.part[r][threadIdx.x]);
-        for (int r = 0; r < ranks; ++r)
-            s.sum += in_units(sm.part[r][threadIdx.x], s.back);
-        Scale sc = scale_of(s);
+        Scale sc = scale_of(sm.sum[threadIdx.x]);
         if (!(sc.unit < INFINITY)) {
             sc = Scale{0, 0.0f};
             sm.bad[threadIdx.x] = 1;
@@ -463,6 +459,9 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
                     if (top > 65504.0f)
                         report(r >> a.log_rows);
                     const uint32_t at = ea + e_at(r, col);
+                    // not unrolled: four blocks' stores at once take longer (32 x 128 x 1024
+                    // bf16 72 us, one after the other 68)
+#pragma unroll 1
                     for (int to_rank = 0; to_rank < ranks; ++to_rank) {
                         const uint32_t far = at_rank(at, to_rank);
                         far_store(far, hi);
