@@ -412,7 +412,7 @@ class _Seq:
         self.recur_step, self.orthogonalize = lib.bstq_recur_step, lib.bstq_orthogonalize
         self.sizes = {"recur": lib.bstq_recur_work_size, "recur_grad": lib.bstq_recur_grad_work_size,
                       "orthogonalize": lib.bstq_orthogonalize_work_size}
-        self.size = functools.lru_cache(maxsize=1024)(lambda where, *shape: int(self.sizes[where](*shape)))
+        self.size = functools.lru_cache(maxsize=1024)(lambda device, where, *shape: int(self.sizes[where](*shape)))
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -488,7 +488,7 @@ def _rows(where, *named):
 
 
 def _workspace(q, where, work, x, *shape):
-    nbytes = q.size(where, *shape)
+    nbytes = q.size(x.get_device(), where, *shape)
     if nbytes == 0:
         raise BstqError(-10, f"bstq_{where}_work_size")
     if work is None:

@@ -37,6 +37,7 @@
 
 #include "../../include/bstq.h"
 #include "bstq_common.h"
+#include "bstq_orth_plan.h"
 #include "bstq_pack.cuh"
 #include "bstq_tensor.cuh"
 
@@ -775,13 +776,45 @@ bool sizes_ok(int64_t batch, int64_t m, int64_t n)
 }
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Whether the small kernel takes the size: 128 rows, and 256 columns for each of
-// up to 16 blocks of a cluster (64 x 4000 float 110 us against 184 in tiles,
-// 3 x 128 x 4096 bf16 83 against 123).
-bool is_small(int64_t m, int64_t n)
+// The widest cluster of the small kernel that the device places; asked once for each.
+// Clusters of 16 are beyond what every device or part of one has room for: there the
+// sizes that need them go in tiles.  Without a device, sizes are those of one that has.
+int widest_cluster()
 {
-    const int64_t p = m < n ? m : n, q = m < n ? n : m;
-    return p <= 128 && q <= 4096;
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return kWidestCluster;
+    }
+    int widest = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (widest)
+        return widest;
+    auto *fn = small_kernel<__nv_bfloat16, 1, 256, true, false>;  // no other takes more shared memory
+    typedef SmallShape<1, 256, true, false> S;
+    static_assert(S::kSmem >= SmallShape<2, 256, true, false>::kSmem, "");
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    widest = 1;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) == cudaSuccess &&
+        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess)
+        for (int blocks = kWidestCluster; blocks > 1 && widest == 1; blocks /= 2) {
+            int clusters = 0;
+            at.val.clusterDim.x = (unsigned)blocks;
+            cfg.gridDim = dim3((unsigned)blocks);
+            if (cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) == cudaSuccess && clusters > 0)
+                widest = blocks;
+        }
+    cudaGetLastError();  // a size that the device has not is no error of the caller's
+    if (dev < 64)
+        known[dev].store(widest, std::memory_order_relaxed);
+    return widest;
 }
 
 struct OrthPlan {
@@ -795,7 +828,7 @@ OrthPlan plan_of(int64_t batch, int64_t m, int64_t n)
     s.ldx = (s.q + 7) & ~7, s.lds = (s.p + 7) & ~7;
     const int64_t want = (m * n + 8191) / 8192;  // four pieces of eight to a thread
     s.parts = (int)(want < 1 ? 1 : (want > kNormMaxParts ? kNormMaxParts : want));
-    if (is_small(m, n)) {
+    if (is_small(m, n, widest_cluster())) {
         s.total = 256;
         return s;
     }
@@ -982,7 +1015,7 @@ cudaError_t run_small(const SmallArgs &a, cudaStream_t s)
                          : launch_small<T, PL, 128, false, false>(a, groups, 1, s);
     if (a.q <= 256)
         return launch_small<T, PL, 256, false, false>(a, groups, 1, s);
-    return launch_small<T, PL, 256, true, false>(a, groups, a.q <= 512 ? 2 : (a.q <= 1024 ? 4 : (a.q <= 2048 ? 8 : 16)), s);
+    return launch_small<T, PL, 256, true, false>(a, groups, cluster_of(a.q), s);
 }
 
 template <typename T>
@@ -991,7 +1024,7 @@ cudaError_t orthogonalize(int64_t batch, int64_t m, int64_t n, const T *G, T *X,
 {
     constexpr int PLANES = PlanesOf<T>::value;
     cudaError_t err;
-    if (is_small(m, n)) {
+    if (is_small(m, n, widest_cluster())) {
         SmallArgs a{};
         a.G = G, a.X = X, a.gb = st[0], a.gr = st[1], a.xb = st[2], a.xr = st[3], a.batch = batch;
         a.tall = m > n, a.p = (int)(a.tall ? n : m), a.q = (int)(a.tall ? m : n), a.steps = steps;

@@ -347,3 +347,27 @@ def test_results_whose_rows_overlap_are_refused():
         for xb, xr in ((24, 6), (25, 6), (6, 18), (30, 7), (40, 6)):
             assert lib.bstq_orthogonalize(0, 3, 4, 6, p, p, (ctypes.c_int64 * 4)(24, 6, xb, xr), 5, None, p,
                                           None) == bstq.ERR_NODEVICE, (xb, xr)
+
+
+def test_sizes_go_in_tiles_where_no_cluster_fits_them(tmp_path):
+    """A device, or a part of one, may place fewer blocks to a cluster than 16:
+    the sizes that need more are not small there (the workspace and the launch
+    ask the same function)."""
+    import os
+    import shutil
+    import subprocess
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("g++ not available")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "orth_plan_check")
+    subprocess.run([gxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-I",
+                    os.path.join(root, "symmetric_tridiagonal_eigensolver_gb300", "csrc"),
+                    os.path.join(root, "tests", "orth_plan_check.cpp"), "-o", exe], check=True)
+    cases = [((128, 4096, 16), (1, 16)), ((4096, 128, 16), (1, 16)), ((128, 4097, 16), (0, 32)), ((129, 200, 16), (0, 1)),
+             ((128, 4097, 32), (0, 32)), ((128, 4096, 8), (0, 16)), ((64, 2048, 8), (1, 8)), ((2049, 64, 8), (0, 16)),
+             ((1, 1024, 4), (1, 4)), ((100, 1025, 4), (0, 8)), ((128, 256, 1), (1, 1)), ((128, 257, 1), (0, 2)),
+             ((1, 1, 1), (1, 1)), ((1 << 20, 1, 16), (0, 4096))]
+    r = subprocess.run([exe], input="".join("%d %d %d\n" % c for c, _ in cases), capture_output=True, text=True, timeout=60,
+                       check=True)
+    assert [tuple(map(int, line.split())) for line in r.stdout.splitlines()] == [want for _, want in cases]
