@@ -316,7 +316,7 @@ int bstq_stedc_leaves(bstq_dtype dtype, bstq_jobz jobz, int n, int leaf, int64_t
  *             where that is none); NULL: not wanted.
  *   work      bstq_recur_work_size(...) bytes of device memory, 256-byte
  *             aligned.  On completion (time > 0) its first int32 is 0, or 1 if a
- *             tile gave up waiting for another (the results are then invalid).
+ *             wait ran out (bstq_set_wait_limit); what depends on it is NaN.
  * time == 0 or lengths[b] == 0 gives hT = h0.  A NaN or infinity in x, r or
  * h0 reaches the later steps of its own channel only.
  * Argument numbers for -k: 1 dtype, 2 batch, 3 time, 4 dim, 5 x, 6 r, 7 rate,
@@ -401,7 +401,7 @@ int bstq_recur_step(bstq_dtype dtype, int64_t batch, int64_t dim, int64_t rows, 
  *             the iterates' singular values must stay below 2.
  *   work      bstq_orthogonalize_work_size(...) bytes of device memory,
  *             256-byte aligned.  On completion its first int32 is 0, or 1 if a
- *             kernel gave up waiting for its own copies (X is then invalid).
+ *             wait ran out (bstq_set_wait_limit); what depends on it is NaN.
  * Argument numbers for -k: 1 dtype, 2 batch, 3 m, 4 n, 5 G, 6 X, 7 strides,
  * 8 steps, 9 coefs, 10 work.
  */
@@ -409,6 +409,13 @@ size_t bstq_orthogonalize_work_size(bstq_dtype dtype, int64_t batch, int64_t m, 
 
 int bstq_orthogonalize(bstq_dtype dtype, int64_t batch, int64_t m, int64_t n, const void *G, void *X,
                        const int64_t *strides, int steps, const float *coefs, void *work, void *stream);
+
+/* Every wait inside a kernel of the recurrence and of the update ends: after this
+ * many cycles of the SM clock the kernel gives up, sets the first int32 of the
+ * workspace to 1 and writes NaN for what it cannot know.  The limit holds for
+ * later calls of the whole process; negative: the default, 4e9 cycles (about two
+ * seconds).  Returns the limit until now. */
+int64_t bstq_set_wait_limit(int64_t cycles);
 
 /* Description of the kernel the library would launch (for tests and
  * benchmarks): fills up to `len` bytes of `buf` with a NUL-terminated string

@@ -32,7 +32,7 @@ EXPORTS = ("bstq_work_size", "bstq_work_size_ex", "bstq_solve", "bstq_solve_ex",
            "bstq_syev_work_size", "bstq_syev", "bstq_stedc_leaves_work_size", "bstq_stedc_leaves",
            "bstq_diag_work_size", "bstq_diag",
            "bstq_recur_work_size", "bstq_recur", "bstq_recur_grad_work_size", "bstq_recur_grad",
-           "bstq_recur_step", "bstq_orthogonalize_work_size", "bstq_orthogonalize")
+           "bstq_recur_step", "bstq_orthogonalize_work_size", "bstq_orthogonalize", "bstq_set_wait_limit")
 
 # Diagnostic ops (bstq_diag): one building block of the solve on a table of
 # inputs; values in and out per record.
@@ -118,6 +118,8 @@ def load(path: str = LIB_PATH):
         lib.bstq_solve_noalloc.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, i64, vp, vp, vp, vp,
                                            vp, P]
         c_int = ctypes.c_int
+        lib.bstq_set_wait_limit.restype = i64
+        lib.bstq_set_wait_limit.argtypes = [i64]
         lib.bstq_recur_work_size.restype = sz
         lib.bstq_recur_work_size.argtypes = [c_int, i64, i64, i64]
         lib.bstq_recur.restype = c_int
@@ -511,7 +513,10 @@ def recur(x, r, rate, h0=None, lengths=None, out=None, work=None, stream=None):
     (default zero).  ``lengths`` (batch,) int32 ends sequences early: h is
     zero beyond.  Returns (h, hT): h in x's dtype (``out`` if given) and the
     last states (batch, dim) float32.  Work is enqueued on ``stream`` (default:
-    torch's current stream); nothing is synchronised."""
+    torch's current stream); nothing is synchronised.  Should a wait inside the
+    kernel run out (two seconds), what depends on it is NaN and the first int32
+    of ``work`` is 1.  The result carries no autograd graph: its gradients come
+    from :func:`recur_grad`."""
     q = _seq or _seq_calls()
     dtype, shape, dev = x.dtype, x.shape, x.get_device()
     code = q.codes.get(dtype)
@@ -556,7 +561,8 @@ def recur_grad(x, r, rate, h, dh, dhT=None, h0=None, lengths=None, work=None, st
     dim) and ``dhT`` (batch, dim) float32 (default zero) the gradients of h and
     hT.  Returns (dx, dr, drate, dh0): dx and dr in x's dtype, zero beyond a
     sequence's length; drate (dim,) and dh0 (batch, dim) float32.  Sums run in
-    a fixed order.  Nothing is synchronised."""
+    a fixed order.  Nothing is synchronised; a wait that runs out leaves NaN, as
+    in :func:`recur`."""
     q = _seq or _seq_calls()
     dtype, shape = x.dtype, x.shape
     code = q.codes.get(dtype)
@@ -643,7 +649,8 @@ def orthogonalize(G, steps: int = 5, coefs=None, out=None, work=None, stream=Non
     ``coefs`` is one (a, b, c) for all steps or one for each (default 3.4445,
     -4.7750, 2.0315).  Returns X in G's dtype (``out`` if given; it may be G
     itself).  A G whose columns are contiguous (a transposed view) gives an X
-    of the same layout.  Nothing is synchronised."""
+    of the same layout.  Nothing is synchronised; a wait that runs out leaves
+    NaN, as in :func:`recur`.  The result carries no autograd graph."""
     q = _seq or _seq_calls()
     dtype, shape = G.dtype, G.shape
     code = q.codes.get(dtype)

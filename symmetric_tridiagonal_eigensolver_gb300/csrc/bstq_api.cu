@@ -6,6 +6,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "../../include/bstq.h"
@@ -52,6 +53,13 @@ int cuda_fail(cudaError_t err, const char *what)
              cudaGetErrorName(err));
     return BSTQ_ERR_CUDA;
 }
+
+namespace {
+constexpr long long kDefaultWait = 4000000000LL;  // about two seconds
+std::atomic<long long> g_wait{kDefaultWait};
+}  // namespace
+
+long long wait_limit() { return g_wait.load(std::memory_order_relaxed); }
 
 // Device properties of the current device, cached per device ordinal.
 bool dev_info(DevInfo &out)
@@ -893,6 +901,11 @@ extern "C" const char *bstq_status_string(int code)
 }
 
 extern "C" const char *bstq_version(void) { return "bstq 0.1.0 sm_103a"; }
+
+extern "C" int64_t bstq_set_wait_limit(int64_t cycles)
+{
+    return g_wait.exchange(cycles < 0 ? kDefaultWait : cycles, std::memory_order_relaxed);
+}
 
 extern "C" const char *bstq_last_error(void) { return g_last_error; }
 

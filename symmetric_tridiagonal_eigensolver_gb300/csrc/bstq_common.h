@@ -18,6 +18,9 @@ struct DevInfo {
 // Properties of the current device (false when there is none).
 bool dev_info(DevInfo &out);
 
+// Cycles after which a kernel's wait gives up (bstq_set_wait_limit).
+long long wait_limit();
+
 // Keeps the text of a CUDA error for bstq_last_error; returns BSTQ_ERR_CUDA.
 int cuda_fail(cudaError_t err, const char *what);
 

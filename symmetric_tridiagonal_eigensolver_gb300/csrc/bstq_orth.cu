@@ -277,6 +277,7 @@ struct ProductArgs {
     long long last_b, last_r;
     int flip, vector;   // write it transposed; its rows' pieces of eight start on 16 bytes
     int *status;
+    long long wait;     // cycles after which a wait gives up
 };
 
 constexpr int kBM = 128, kBK = 64;
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     using S = Shape<BN, PLANES, CTAS>;
     constexpr bool UPPER = EPI == EPI_GRAM || EPI == EPI_SQUARE;
     extern __shared__ char raw[];
-    __shared__ uint64_t bars[2 * S::kStages + 4];
+    __shared__ uint64_t bars[2 * S::kStages + 5];
     __shared__ uint32_t tmem_slot;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t bar0 = smem_u32(bars);
@@ -512,6 +513,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     auto empty = [&](int s) { return bar0 + 8u * (S::kStages + s); };
     auto tfull = [&](int s) { return bar0 + 8u * (2 * S::kStages + s); };
     auto tempty = [&](int s) { return bar0 + 8u * (2 * S::kStages + 2 + s); };
+    const uint32_t issued = bar0 + 8u * (2 * S::kStages + 4);  // all products are done
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0 && lane == 0) {
@@ -523,6 +525,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             mbar_init(tfull(s), 1);
             mbar_init(tempty(s), CTAS * kEpiWarps);
         }
+        mbar_init(issued, 1);
         mbar_init_fence();
     }
     if (warp == 2)
@@ -553,7 +556,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 tile_at<BN, CTAS, UPPER>(a, (int)(t - b * a.tiles), i, j);
                 bool ok = true;
                 for (int k = 0; k < steps && ok; ++k) {
-                    if (!mbar_wait(empty(s), phase ^ 1)) {
+                    if (!mbar_wait(empty(s), phase ^ 1, a.wait)) {
                         *a.status = 1;
                         ok = false;
                         break;
@@ -590,6 +593,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 if (!ok)
                     break;
             }
+            // no copy is still on its way in when the block ends, whoever gave up
+            if (rank == 0)
+                for (int k = 0; k < S::kStages; ++k)
+                    mbar_wait(full(k), k < s ? phase : phase ^ 1);
         }
     } else if (warp == 1) {
         if (rank == 0 && elect_one()) {
@@ -603,12 +610,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 for (int k = 0; k < steps; ++k) {
                     const bool first = k % S::kChunk == 0;
                     if (first) {
-                        if (!(ok = mbar_wait(tempty(acc), aphase ^ 1)))
+                        if (!(ok = mbar_wait(tempty(acc), aphase ^ 1, a.wait)))
                             break;
                         tc_after();
                     }
                     const uint32_t d = tmem + acc * BN;
-                    if (!(ok = mbar_wait(full(s), phase)))
+                    if (!(ok = mbar_wait(full(s), phase, a.wait)))
                         break;
                     tc_after();
                     const uint32_t at = base + s * S::kStage, bt = at + PLANES * S::kA;
@@ -638,6 +645,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             }
             if (!ok)
                 *a.status = 1;
+            tc_commit<CTAS>(issued);  // nor any product
+            mbar_wait(issued, 0);
+        } else if (rank == 1 && elect_one()) {
+            mbar_wait(issued, 0);  // nor an arrival from the other block
         }
     } else if (warp >= 4) {
         // warp w reads lanes 32 (w mod 4) and up, and one half of the columns
@@ -653,24 +664,33 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         };
         int acc = 0, side = 0;
         uint32_t aphase = 0;
+        // Where a wait ran out, in this product or in one before, the result is no
+        // number; a warp that gave up goes on without waiting or handing on.
+        const bool wrong = EPI == EPI_LAST && __ldcg(a.status) != 0;
+        bool ok = true;
+        auto sums_there = [&] {
+            if (ok && !__all_sync(0xffffffffu, mbar_wait(tfull(acc), aphase, a.wait))) {
+                *(volatile int *)a.status = 1;
+                ok = false;
+            }
+            tc_after();
+        };
         for (long long t = tile0; t < total; t += tiles_by) {
             const long long b = t / a.tiles;
             int i, j;
             tile_at<BN, CTAS, UPPER>(a, (int)(t - b * a.tiles), i, j);
             i = i * CTAS + rank;  // this block's 128 rows
-            const float unit = a.unit ? __ldcg(a.unit + b) : 1.0f / kXs;
+            const float stored = a.unit ? __ldcg(a.unit + b) : 1.0f / kXs;
             const int row = i * kBM + quarter * 32 + lane, col = j * BN + half * (BN / 2);
             // of the symmetric ones a square of 128 above the diagonal goes to both
             // places, one on it to its own, one below is another tile's
             auto wanted = [&](int c) { return !UPPER || (col + 32 * c) / kBM >= i; };
             auto mirror = [&](int c) { return UPPER && (col + 32 * c) / kBM > i; };
-            bool ok = true;
             Before<PLANES, EPI> before;
             before.load(a, b, row, col);
             if (PLANES == 1) {
-                if (!(ok = mbar_wait(tfull(acc), aphase)))
-                    break;
-                tc_after();
+                sums_there();
+                const float unit = wrong || !ok ? nanf("") : stored;
 #pragma unroll 1
                 for (int c = 0; c < C; ++c) {
                     float f[32];
@@ -688,7 +708,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0)
+                if (ok && lane == 0)
                     leave(acc);
                 if (++acc == 2)
                     acc = 0, aphase ^= 1;
@@ -700,9 +720,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     for (int k = 0; k < 16; ++k)
                         sum[c][k] = pk_all<2>(0.0f);
                 for (int k = 0; k < steps; k += S::kChunk) {
-                    if (!(ok = mbar_wait(tfull(acc), aphase)))
-                        break;
-                    tc_after();
+                    sums_there();
                     const bool last = k + S::kChunk >= steps;
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
@@ -722,14 +740,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                     }
                     tc_before();
                     __syncwarp();
-                    if (lane == 0)
+                    if (ok && lane == 0)
                         leave(acc);
                     if (++acc == 2)
                         acc = 0, aphase ^= 1;
                 }
                 side ^= 1;
-                if (!ok)
-                    break;
+                const float unit = wrong || !ok ? nanf("") : stored;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     if (c)
@@ -1029,7 +1046,7 @@ cudaError_t orthogonalize(int64_t batch, int64_t m, int64_t n, const T *G, T *X,
         a.G = G, a.X = X, a.gb = st[0], a.gr = st[1], a.xb = st[2], a.xr = st[3], a.batch = batch;
         a.tall = m > n, a.p = (int)(a.tall ? n : m), a.q = (int)(a.tall ? m : n), a.steps = steps;
         a.log_rows = a.p > 64 ? 7 : (a.p > 32 ? 6 : (a.p > 16 ? 5 : 4));
-        a.status = (int *)work;
+        a.status = (int *)work, a.wait = wait_limit();
         const int lead = 16 / (int)sizeof(T);
         a.vector = !misaligned_to(G, 16) && st[1] % lead == 0 && st[0] % lead == 0;
         a.vector_out = !a.tall && !misaligned_to(X, 16) && st[3] % lead == 0 && st[2] % lead == 0;
@@ -1067,6 +1084,7 @@ cudaError_t orthogonalize(int64_t batch, int64_t m, int64_t n, const T *G, T *X,
         const float theta = k == steps - 1 ? 1.0f : (k == steps - 2 ? 0.5f : 0.0f);
         ProductArgs a{};
         a.p = pl.p, a.q = pl.q, a.ldx = pl.ldx, a.lds = pl.lds, a.batch = batch, a.status = (int *)work;
+        a.wait = wait_limit();
         a.unit = k == 0 ? unit : nullptr;
         const int from = k & 1, to = from ^ 1;
         a.k = pl.q, a.c0 = theta;

@@ -38,6 +38,7 @@ struct SmallArgs {
     int vector, vector_out;  // whether pieces of eight of G and of X start on 16 bytes
     float coefs[3 * 32];
     int *status;
+    long long wait;  // cycles after which a wait gives up
 };
 
 template <int PL, int QC, bool CL, bool STACK>
@@ -64,8 +65,8 @@ struct SmallShared {
     float warp[16], part[16][8];  // [rank][matrix]
     Sq sum[8];
     Scale scale[8];
-    int bad[8];
-    uint64_t done;
+    int bad[8], stop;
+    uint64_t done, drained;
     uint32_t tmem;
 };
 
@@ -138,10 +139,13 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
 
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&sm.done), 1);
+        mbar_init(smem_u32(&sm.drained), 1);
         mbar_init_fence();
     }
     if (threadIdx.x < 8)
         sm.bad[threadIdx.x] = 0;
+    if (threadIdx.x == 0)
+        sm.stop = 0;
     if (warp == 0)
         tmem_alloc(smem_u32(&sm.tmem), S::kCols);
     if (blockIdx.x == 0 && threadIdx.x == 0)
@@ -293,12 +297,6 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const bool real = (row & (rows - 1)) < a.p;
     uint32_t phase = 0;
-    auto finish = [&] {  // every thread: the products issued last are done
-        if (!mbar_wait(done, phase))
-            *a.status = 1;
-        phase ^= 1;
-        tc_after();
-    };
     // A product added to a sum costs it a rounding towards zero: the 16 of X X^T in
     // 256 columns go to two sums (4 x 128 x 512 normal float: 1.2e-6 off instead of
     // 1.7e-6, 64 x 4000 2.8e-6 instead of 3.2e-6).
@@ -334,6 +332,28 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
         } else {
             sm.bad[matrix] = 1;
         }
+    };
+    // Every thread: the products issued last are done, or a wait ran out: then the block
+    // goes on without waiting, its results are no numbers, nor those of the blocks that
+    // still get something from it (`shared`).
+    auto finish = [&](bool shared) {
+        if (!mbar_try(done, phase)) {
+            const long long start = clock64();
+            while (!mbar_try(done, phase) && *(volatile int *)&sm.stop == 0)
+                if (clock64() - start > a.wait) {
+                    for (int m = 0; m < stacked; ++m) {
+                        if (shared)
+                            report(m);
+                        sm.bad[m] = 1;
+                    }
+                    __threadfence_block();
+                    *(volatile int *)&sm.stop = 1;
+                    *(volatile int *)a.status = 1;
+                }
+            __threadfence_block();
+        }
+        phase ^= 1;
+        tc_after();
     };
     // Eight values of X X^T, columns col and up of row r, to E times its scale:
     // `f` for both, `theta` off the diagonal's element.
@@ -391,7 +411,7 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
         if (CL) {
             // the partial sums in this block's memory: the others have read the
             // last ones, and this block is done with its B
-            finish();
+            finish(true);
             const int per = 128 / ranks;
             const int beside = S::kBeside ? S::kE : 0;
             float *const to = reinterpret_cast<float *>(es + beside) + row * 128;
@@ -475,7 +495,7 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
             cluster_wait();
             fence_async_smem();
         } else {
-            finish();
+            finish(true);
             float top = 0.0f;
             const Pk<2> scale_e = e_scale(mi);
             for (int n = part; n < pieces32; n += kParts) {
@@ -513,7 +533,7 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
             tc_commit(done);
         }
         __syncwarp();
-        finish();
+        finish(!last);
         const float b0c = (cb + 2.0f * cc * theta) * (kBs / kEs), b1c = cc * (kBs / kEs / kEs);
         float top = 0.0f;
         for (int n = part; n < pieces32; n += kParts) {
@@ -556,7 +576,7 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
             tc_commit(done);
         }
         __syncwarp();
-        finish();
+        finish(!last);
         const float x0 = ca + theta * (cb + theta * cc), unit = unit_of(mi);
         const float scale = last ? unit : unit * kXs;
         const long long b = b0 + mi;
@@ -603,8 +623,14 @@ __global__ void __launch_bounds__(SmallShape<PL, QC, CL, STACK>::kThreads, Small
         __syncthreads();
         tc_after();
     }
-    if (warp == 0)
+    if (warp == 0) {
+        if (elect_one() && sm.stop) {  // the last products may still run
+            tc_commit(smem_u32(&sm.drained));
+            mbar_wait(smem_u32(&sm.drained), 0);
+        }
+        __syncwarp();
         tmem_free(tmem, S::kCols);
+    }
 }
 
 }  // namespace

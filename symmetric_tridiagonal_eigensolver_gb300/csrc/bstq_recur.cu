@@ -204,6 +204,7 @@ struct RecurArgs {
     unsigned long long *maps;
     unsigned long long *states;  // two channels to a word, [chain][group][32]
     int *status;
+    long long wait;  // cycles after which a wait gives up
 };
 
 struct RecurMaps {  // TMA: inputs x, r (h, dh), outputs h or dx, dr
@@ -250,23 +251,34 @@ constexpr int tile_smem()
 static_assert(3 * (tile_smem<float, false>() + 1024) <= 228 * 1024 && 2 * (tile_smem<float, true>() + 1024) <= 228 * 1024,
               "the blocks of an SM");
 
-// A wait that ends: with its barrier, after two seconds, or when another ended so.
+// A wait that ends: with its barrier (true), after two seconds, or when another ended so
+// (false).  From then on the block's barriers may complete too early, for its warps go
+// on arriving.  But `stop` is set before, and who waits for such an arrival sees it: so a
+// thread that reads stop == 0 after a wait has what it waited for, and one that reads 1
+// has no number, gives NaN on and writes nothing that others may still read.
 template <int W>
-__device__ __forceinline__ void wait_for(TileShared<W> &sm, uint64_t &bar, uint32_t parity, int *status)
+__device__ __forceinline__ bool wait_for(TileShared<W> &sm, uint64_t &bar, uint32_t parity, const RecurArgs &a)
 {
     const uint32_t at = smem_u32(&bar);
     if (mbar_try(at, parity))
-        return;
+        return true;
     const long long start = clock64();
     while (!mbar_try(at, parity)) {
         if (*(volatile int *)&sm.stop)
-            return;
-        if (clock64() - start > kWaitCycles) {
+            return false;
+        if (clock64() - start > a.wait) {
             *(volatile int *)&sm.stop = 1;
-            *(volatile int *)status = 1;
+            *(volatile int *)a.status = 1;
         }
     }
+    return true;
 }
+template <int W>
+__device__ __forceinline__ bool stopped(const TileShared<W> &sm)
+{
+    return *(const volatile int *)&sm.stop != 0;
+}
+__device__ __forceinline__ float no_number() { return __int_as_float(0x7fffffff); }
 
 __device__ __forceinline__ unsigned long long load_mark(const unsigned long long *p)
 {
@@ -361,11 +373,11 @@ __device__ __forceinline__ bool read_maps(const unsigned long long *at, int n, M
 // leaves the entering state for the others, publishes the tile's map (or that of
 // its four tiles, or the state after its group) and returns the state after the
 // tile.  `first` is the channels' first tile, `last` their last.  `between` runs
-// when every warp has its map.
+// when every warp has its map.  `dead`: this thread has no numbers any more.
 template <bool GRAD, int W, typename F>
 __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int slot, uint32_t phase, int chain_id, int rank,
                                       int first, int last, const float *start, const bool (&on)[2], F between,
-                                      float (&enter)[2], float (&after)[2])
+                                      float (&enter)[2], float (&after)[2], bool &dead)
 {
     const int lane = threadIdx.x & 31;
     const int group = rank / a.group, groups = (a.ranks + a.group - 1) / a.group;
@@ -382,7 +394,8 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
     bool have_near = single == rank, entered = false, mine = false;
     const uint32_t ready = smem_u32(&sm.ready[slot]);
     auto leave = [&] {
-        *reinterpret_cast<float2 *>(&sm.enter[slot][2 * lane]) = make_float2(enter[0], enter[1]);
+        if (!dead)
+            *reinterpret_cast<float2 *>(&sm.enter[slot][2 * lane]) = make_float2(enter[0], enter[1]);
         __syncwarp();
         if (lane == 0)
             mbar_arrive(smem_u32(&sm.entered[slot]));
@@ -405,7 +418,7 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
     do {
         if (!have_near && read_maps(singles + (long long)single * kChannels, rank - single, near)) {
             have_near = true;
-            if (mine && rank - four == 3)
+            if (mine && !dead && rank - four == 3)
                 publish();
         }
         if (!entered) {
@@ -434,6 +447,7 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
         // with the entering state known there is nothing to do but sleep
         if (!mine && __all_sync(0xffffffffu, entered ? mbar_try(ready, phase) : mbar_test(ready, phase))) {
             mine = true;
+            dead = stopped(sm) || dead;
             between();
             if (!EARLY && entered)
                 leave();
@@ -444,18 +458,30 @@ __device__ __forceinline__ void chain(const RecurArgs &a, TileShared<W> &sm, int
                 const float mq[2] = {wq.x, wq.y}, mv[2] = {wv.x, wv.y};
                 own.then(mq, mv);
             }
-            if (maps && (have_near || rank - four < 3))
+            if (maps && !dead && (have_near || rank - four < 3))
                 publish();
         }
         if (entered && mine)
             break;
         if (t0 == 0)
             t0 = clock64();
-        if (clock64() - t0 > kWaitCycles) {
+        if (clock64() - t0 > a.wait) {
             *(volatile int *)&sm.stop = 1;
             *(volatile int *)a.status = 1;
         }
-    } while (__any_sync(0xffffffffu, *(volatile int *)&sm.stop == 0));
+    } while (__any_sync(0xffffffffu, !stopped(sm)));
+    if (!entered || !mine)
+        dead = true;
+    if (dead) {  // told to those who wait for the tile, too
+        enter[0] = enter[1] = after[0] = after[1] = no_number();
+        const int block = rank / 4;
+        for (int c = 0; c < 2 && maps; ++c) {
+            publish_map(singles + (long long)rank * kChannels + c, no_number(), no_number());
+            publish_map(fours + (long long)block * kChannels + c, no_number(), no_number());
+        }
+        publish_states(states + (long long)group * (kChannels / 2), no_number(), no_number());
+        return;
+    }
     after[0] = own.of(0, enter[0]);
     after[1] = own.of(1, enter[1]);
     if (rank < last && rank % a.group == a.group - 1)
@@ -678,13 +704,13 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
         // the tile before, whose sums of dz s are whole once every warp has come
         // to the next one
         Place before{};
-        bool any = false;
+        bool any = false, dead = false;
         auto sums = [&] {
             if (GRAD && any)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int j = before.j0 + 2 * lane + k;
-                    float sum = 0.0f;
+                    float sum = dead ? no_number() : 0.0f;
                     if (holds(before))
 #pragma unroll
                         for (int w = 0; w < S::W; ++w)
@@ -702,14 +728,15 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
                 float enter[2], after[2];
                 // the sums have one place: no warp gets to its next ones before they are read
                 chain<GRAD, S::W>(a, sm, slot, phase, c.ch, c.rank, c.first, c.last, from ? from + at : nullptr, on, sums,
-                             enter, after);
+                                  enter, after, dead);
                 if (c.rank == c.last && to)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         if (on[k])
                             to[at + k] = c.n ? after[k] : enter[k];
             } else {
-                wait_for(sm, sm.ready[slot], phase, a.status);  // keeps the phases in step
+                wait_for(sm, sm.ready[slot], phase, a);  // keeps the phases in step
+                dead = stopped(sm) || dead;
                 sums();
                 __syncwarp();
                 if (lane == 0)
@@ -721,7 +748,8 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
             phase ^= slot;
         }
         if (GRAD) {
-            wait_for(sm, sm.ready[slot], phase, a.status);
+            wait_for(sm, sm.ready[slot], phase, a);
+            dead = stopped(sm) || dead;
             sums();
         }
         return;
@@ -738,15 +766,19 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
         }
         return pk<2>(v);
     };
+    // whether this thread has had all that it waited for, and the next tile's rows were
+    // asked for
+    bool ok = true, asked = false;
     // a warp's rows of a tile into a stage that holds its own results of the
     // tile before last, stored by then
     auto load = [&](const Place &p, int slot) {
+        asked = ok && holds(p);
         if (!holds(p))
             return;
         T *stage = (T *)(stages + slot * S::STAGE);
         if (!TMA) {
             load_rows<T, GRAD>(a, p, stage, warp, lane);
-        } else if (lane == 0) {
+        } else if (lane == 0 && asked) {
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             tma_rows<T, GRAD>(a, maps, p, stage, warp, sm.full[slot][warp]);
         }
@@ -762,7 +794,11 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
         T *stage = (T *)(stages + slot * S::STAGE);
         if (TMA) {
             if (holds(p)) {
-                wait_for(sm, sm.full[slot][warp], loaded[slot], a.status);
+                if (asked && !wait_for(sm, sm.full[slot][warp], loaded[slot], a)) {
+                    ok = false;
+                    if (lane == 0)  // the copy may not land on the results, nor after the block
+                        mbar_wait(smem_u32(&sm.full[slot][warp]), loaded[slot]);
+                }
                 loaded[slot] ^= 1;
             }
         } else {
@@ -777,8 +813,10 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
             Pk<2> z, v;
             l.first(rate, z, v);
             const Pk<2> qw = GRAD ? decay(z) : one_minus_exp<2>(z);
-            put2(&sm.q[slot][warp][2 * lane], qw);
-            put2(&sm.v[slot][warp][2 * lane], v);
+            if (ok) {
+                put2(&sm.q[slot][warp][2 * lane], qw);
+                put2(&sm.v[slot][warp][2 * lane], v);
+            }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_u32(&sm.ready[slot]));
@@ -796,9 +834,12 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
                 }
                 h0 = pk<2>(f);
             }
-            wait_for(sm, sm.ready[slot], phase, a.status);
-            wait_for(sm, sm.entered[slot], phase, a.status);
+            wait_for(sm, sm.ready[slot], phase, a);
+            wait_for(sm, sm.entered[slot], phase, a);
+            ok = ok && !stopped(sm);
             Pk<2> e = get2(&sm.enter[slot][2 * lane]);
+            if (!ok)
+                e = pk_all<2>(no_number());
             for (int w = 0; w < warp; ++w) {
                 const Pk<2> m = get2(&sm.q[slot][w][2 * lane]);
                 e = add_(GRAD ? kept(m, e) : fma_(neg_<2>(m), e, e), get2(&sm.v[slot][w][2 * lane]));
@@ -818,7 +859,8 @@ __global__ void __launch_bounds__(Tile<T, GRAD>::THREADS, Tile<T, GRAD>::BLOCKS)
                 load(next, slot ^ 1);
                 next_rate = rates(next);
             }
-            wait_for(sm, sm.entered[slot], phase, a.status);
+            wait_for(sm, sm.entered[slot], phase, a);
+            ok = ok && !stopped(sm);
             if (TMA && lane == 0)
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             __syncwarp();
@@ -1059,6 +1101,7 @@ cudaError_t run_tiles(bstq_dtype dtype, RecurArgs a, const RecurPlan &p, char *w
     using S = Tile<T, GRAD>;
     a.ranks = (int)p.ranks, a.cols = (int)p.cols, a.chains = (int)p.chains;
     a.status = (int *)work;
+    a.wait = wait_limit();
     a.maps = (unsigned long long *)(work + p.maps);
     a.part = (float *)(work + p.part);
     RecurMaps maps;

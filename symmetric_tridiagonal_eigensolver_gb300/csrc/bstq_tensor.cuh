@@ -62,13 +62,13 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 // on something that never comes ends with its status set instead of hanging.
 constexpr long long kWaitCycles = 4000000000LL;
 
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, long long cycles = kWaitCycles)
 {
     if (mbar_try(bar, parity))
         return true;
     const long long start = clock64();
     while (!mbar_try(bar, parity))
-        if (clock64() - start > kWaitCycles)
+        if (clock64() - start > cycles)
             return false;
     return true;
 }

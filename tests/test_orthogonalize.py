@@ -371,3 +371,30 @@ def test_sizes_go_in_tiles_where_no_cluster_fits_them(tmp_path):
     r = subprocess.run([exe], input="".join("%d %d %d\n" % c for c, _ in cases), capture_output=True, text=True, timeout=60,
                        check=True)
     assert [tuple(map(int, line.split())) for line in r.stdout.splitlines()] == [want for _, want in cases]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("batch,m,n", [(30, 64, 64), (3, 100, 900), (2, 128, 4000), (1, 150, 200), (2, 300, 260)])
+def test_a_wait_that_runs_out_leaves_no_wrong_numbers(batch, m, n, dtype):
+    """With no cycles to wait, whether a wait runs out is up to the products' time:
+    the status says it, and each result is right or NaN."""
+    import torch
+    lib = bstq.load()
+    G = matrices(batch, m, n, dtype, seed=2)
+    want = bstq.orthogonalize(G)
+    code = {"float32": bstq.F32, "bfloat16": bstq.BF16}[dtype]
+    work = torch.zeros(lib.bstq_orthogonalize_work_size(code, batch, m, n), dtype=torch.uint8, device="cuda")
+    status = work[:4].view(torch.int32)
+    torch.cuda.synchronize()
+    before = lib.bstq_set_wait_limit(0)
+    try:
+        for _ in range(3):
+            X = bstq.orthogonalize(G, work=work)
+            torch.cuda.synchronize()
+            gone = torch.isnan(X)
+            assert bool((gone | (X == want)).all())
+            assert int(status) == 1 or not bool(gone.any())
+    finally:
+        lib.bstq_set_wait_limit(before)
+    assert torch.equal(bstq.orthogonalize(G, work=work), want) and int(status) == 0

@@ -794,3 +794,59 @@ def test_a_context_with_a_part_of_the_sms(B, T, D, dtype):
     for u, v, kind in zip(mine, grads, (dtype, dtype, "float32", "float32")):
         top = float(v.abs().max())
         near(u, f64(v), (64 + 16 * (B * T) ** 0.5) * U * 4 * top, kind)
+
+
+# --------------------------------------------------------------------------
+# Waits that run out
+# --------------------------------------------------------------------------
+
+def nan_or_equal(got, want):
+    import torch
+    return bool((torch.isnan(got) | (got == want)).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("B,T,D", [(1, 20000, 64), (1, 9000, 70), (6, 2500, 1024), (3, 700, 10000)])
+def test_a_wait_that_runs_out_leaves_no_wrong_numbers(B, T, D, dtype):
+    """With no cycles to wait, tiles give up on what the others have not published
+    yet: the status says so, and every output is right or NaN."""
+    import torch
+    lib = bstq.load()
+    make, g = problem(B, T, D, dtype, seed=1)
+    x, r, dh = make(B, T, D), make(B, T, D), make(B, T, D)
+    rate = torch.from_numpy(chain_rates(D)).cuda() + 0.01
+    h0 = torch.randn(B, D, generator=g).cuda()
+    lengths = torch.tensor([T - 7 * b for b in range(B)], dtype=torch.int32, device="cuda")
+    kw = dict(h0=h0, lengths=lengths)
+    want = bstq.recur(x, r, rate, **kw)
+    grads = bstq.recur_grad(x, r, rate, want[0], dh, **kw)
+    code = {"float32": bstq.F32, "bfloat16": bstq.BF16}[dtype]
+    work = torch.zeros(max(lib.bstq_recur_work_size(code, B, T, D), lib.bstq_recur_grad_work_size(code, B, T, D)),
+                       dtype=torch.uint8, device="cuda")
+    status = work[:4].view(torch.int32)
+    torch.cuda.synchronize()
+    before = lib.bstq_set_wait_limit(0)
+    try:
+        for call, right in ((lambda: bstq.recur(x, r, rate, work=work, **kw), want),
+                            (lambda: bstq.recur_grad(x, r, rate, want[0], dh, work=work, **kw), grads)):
+            outs = call()
+            torch.cuda.synchronize()
+            gave_up = int(status)
+            assert all(nan_or_equal(u, v) for u, v in zip(outs, right))
+            missing = any(bool(torch.isnan(u).any()) for u in outs)
+            assert gave_up == 1 and missing
+    finally:
+        assert lib.bstq_set_wait_limit(before) == 0
+    again = bstq.recur(x, r, rate, work=work, **kw)
+    assert int(status) == 0 and all(torch.equal(u, v) for u, v in zip(again, want))
+    again = bstq.recur_grad(x, r, rate, want[0], dh, work=work, **kw)
+    assert int(status) == 0 and all(torch.equal(u, v) for u, v in zip(again, grads))
+
+
+def test_the_wait_limit_is_kept_and_given_back():
+    lib = _lib()
+    default = lib.bstq_set_wait_limit(7)
+    assert default == 4000000000
+    assert lib.bstq_set_wait_limit(-1) == 7
+    assert lib.bstq_set_wait_limit(0) == default and lib.bstq_set_wait_limit(-5) == 0
