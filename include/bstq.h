@@ -397,8 +397,10 @@ int bstq_recur_step(bstq_dtype dtype, int64_t batch, int64_t dim, int64_t rows, 
  *   coefs     host memory, (a, b, c) of each step; NULL: 3.4445, -4.7750,
  *             2.0315 at every step, which in five steps takes singular values
  *             of X_0 from 0.0016 upwards to between 0.68 and 1.21.  Magnitudes
- *             up to 16;
- *             the iterates' singular values must stay below 2.
+ *             up to 16 for a and 32 for b and c, which schedules with a steep
+ *             first step need (8.3, -23.6, 17.3).  The iterates' singular values
+ *             must stay below 2 and those of b A + c A^2 below 60: fp16 ends
+ *             there, and the result is NaN.
  *   work      bstq_orthogonalize_work_size(...) bytes of device memory,
  *             256-byte aligned.  On completion its first int32 is 0, or 1 if a
  *             wait ran out (bstq_set_wait_limit); what depends on it is NaN.

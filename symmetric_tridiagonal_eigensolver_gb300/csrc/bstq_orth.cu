@@ -1146,7 +1146,7 @@ extern "C" int bstq_orthogonalize(bstq_dtype dtype, int64_t batch, int64_t m, in
     float c[3 * kMaxSteps];
     for (int i = 0; i < 3 * steps; ++i) {
         c[i] = coefs ? coefs[i] : kCoefs[i % 3];
-        if (!(fabsf(c[i]) <= 16.0f))
+        if (!(fabsf(c[i]) <= (i % 3 ? 32.0f : 16.0f)))
             return -9;
     }
     if (!work || misaligned_to(work, 256))

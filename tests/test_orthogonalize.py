@@ -398,3 +398,38 @@ def test_a_wait_that_runs_out_leaves_no_wrong_numbers(batch, m, n, dtype):
     finally:
         lib.bstq_set_wait_limit(before)
     assert torch.equal(bstq.orthogonalize(G, work=work), want) and int(status) == 0
+
+
+STEEP = [(8.3, -23.6, 17.3), (4.1, -2.9, 0.55), (3.9, -2.8, 0.5), (3.3, -2.4, 0.46), (2.3, -1.6, 0.4)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("m,n", [(64, 64), (100, 700), (300, 260)])
+def test_a_schedule_with_a_steep_first_step(m, n, dtype):
+    """Coefficients above 16 in b and c.  Roundings of the start grow by the product
+    of the a (1007 instead of 484), those of the products by |b A + c A^2| <= 8.05
+    instead of 2.75."""
+    G = matrices(2, m, n, dtype, seed=11, kind="normal")
+    X = bstq.orthogonalize(G, coefs=STEEP).double().cpu().numpy()
+    want = reference(G.double().cpu().numpy(), STEEP)
+    later = 8.05 / 2.75 * (32 * 2.0 ** -21 if dtype == "float32" else 1.1e-2)
+    lim = 1007 * 2.0 ** -22 / min(m, n) ** 0.5 + later + (0 if dtype == "float32" else 2.0 ** -9)
+    assert np.linalg.norm(X - want) <= lim * np.linalg.norm(want)
+
+
+def test_limits_of_the_coefficients():
+    import os
+    if not os.path.exists(bstq.LIB_PATH):
+        from symmetric_tridiagonal_eigensolver_gb300 import build
+        build.build()
+    lib = bstq.load()
+    buf = (ctypes.c_char * 4096)()
+    p = ctypes.c_void_p(ctypes.addressof(buf) + (-ctypes.addressof(buf)) % 256)
+    import torch
+    for row, code in (((16.5, 0, 0), -9), ((0, 32.5, 0), -9), ((0, 0, -32.5), -9), ((0, 0, float("inf")), -9),
+                      ((8.3, -23.6, 17.3), bstq.ERR_NODEVICE), ((16, 32, -32), bstq.ERR_NODEVICE)):
+        if code != -9 and torch.cuda.is_available():
+            continue  # these pointers are no device memory
+        c = (ctypes.c_float * 3)(*row)
+        assert lib.bstq_orthogonalize(0, 2, 4, 6, p, p, None, 1, c, p, None) == code, row
