@@ -1,8 +1,10 @@
 """A recurrent layer whose states are coupled along a chain, trained and served.
 
-The layer's linear system h' = -s (T h - ...) has a symmetric tridiagonal T (a
-chain of diffusing cells).  bstq.solve diagonalises T once; in T's eigenbasis the
-system is bstq.recur with the eigenvalues as rates, one gated channel each.
+The layer starts from the linear system h' = -T (h - x) of a chain of diffusing
+cells, whose T is symmetric and tridiagonal.  bstq.solve diagonalises T once; in
+T's eigenbasis the system is bstq.recur with the eigenvalues as rates.  From there
+the layer is its own model: a gate for each channel, and rates that are trained
+while the basis stays (Q diag(rate) Q^T keeps T's eigenvectors, not its zeros).
 Training runs the recurrence, its gradients (bstq.recur_grad) and, for the two
 weight matrices, updates that bstq.orthogonalize makes orthogonal.  Serving
 starts from the states after a prompt and goes token by token (bstq.recur_step).

@@ -289,10 +289,12 @@ int bstq_stedc_leaves(bstq_dtype dtype, bstq_jobz jobz, int n, int leaf, int64_t
                       void *stream, const bstq_params *p);
 
 /*
- * Gated linear recurrence: what a linear system h' = -T (h - x) with a
- * symmetric tridiagonal T becomes in T's eigenbasis, channel by channel, when
- * the time between two tokens is gated.  Per sequence b and channel j, with
- * sigma the logistic function and lambda+ = max(lambda, 0):
+ * Gated linear recurrence.  A linear system h' = -T (h - x) with a symmetric
+ * tridiagonal T separates in T's eigenbasis into channels with T's eigenvalues
+ * as rates; over a token that lasts s_t it is the recurrence below with one r
+ * for all channels.  The operator takes a gate for each channel, which goes
+ * beyond any one such system.  Per sequence b and channel j, with sigma the
+ * logistic function and lambda+ = max(lambda, 0):
  *
  *     s_t = sigma(r_t)             the step, in (0, 1)
  *     a_t = exp(-lambda+_j s_t)    the decay over it
@@ -318,7 +320,10 @@ int bstq_stedc_leaves(bstq_dtype dtype, bstq_jobz jobz, int n, int leaf, int64_t
  *             aligned.  On completion (time > 0) its first int32 is 0, or 1 if a
  *             wait ran out (bstq_set_wait_limit); what depends on it is NaN.
  * time == 0 or lengths[b] == 0 gives hT = h0.  A NaN or infinity in x, r or
- * h0 reaches the later steps of its own channel only.
+ * h0 reaches the later steps of its own channel only, as a NaN or an infinity.
+ * A state is right to some 2^-24 of the largest |x| and |h0| on its way (more
+ * over long sequences), which is not its own size where it has decayed far
+ * below them; x - h has to stay within float's range.
  * Argument numbers for -k: 1 dtype, 2 batch, 3 time, 4 dim, 5 x, 6 r, 7 rate,
  * 8 h0, 9 lengths, 10 h, 11 hT, 12 strides, 13 work.
  */
@@ -337,6 +342,9 @@ int bstq_recur(bstq_dtype dtype, int64_t batch, int64_t time, int64_t dim, const
  *     dr_t = dz_t lambda+ s_t (1 - s_t)
  *     drate = sum over b and t of dz_t s_t          (0 where rate <= 0)
  *     dh0 = a_0 g_0
+ *
+ * a, 1 - a, s and 1 - s are each right to their own size, however far a gate or
+ * a rate saturates.
  *
  *   h         the forward call's output, as stored.
  *   dhT, h0, lengths   may be NULL (zero, zero, all `time`).
@@ -400,7 +408,7 @@ int bstq_recur_step(bstq_dtype dtype, int64_t batch, int64_t dim, int64_t rows, 
  *             up to 16 for a and 32 for b and c, which schedules with a steep
  *             first step need (8.3, -23.6, 17.3).  The iterates' singular values
  *             must stay below 2 and those of b A + c A^2 below 60: fp16 ends
- *             there, and the result is NaN.
+ *             there, and the result is not finite.
  *   work      bstq_orthogonalize_work_size(...) bytes of device memory,
  *             256-byte aligned.  On completion its first int32 is 0, or 1 if a
  *             wait ran out (bstq_set_wait_limit); what depends on it is NaN.

@@ -24,8 +24,8 @@
 // 2^10 B, which leaves room for singular values up to 2.  The factors of the
 // products are the leading terms alone for bf16 (11 bits, eight times finer
 // than the result) and both terms, in three products, for float and half.
-// X_0 is G times a power of two, exactly; 1 / |G| enters as a factor of sums in
-// the first step, so that no rounding of the input is amplified.
+// X_0 is G times a power of two (bf16 and half exactly, float to 22 bits); 1 / |G|
+// enters as a factor of sums in the first step, so that no rounding by it is amplified.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

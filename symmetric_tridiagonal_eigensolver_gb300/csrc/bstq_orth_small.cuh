@@ -20,8 +20,8 @@
 // What bounds it: the chain of three products a step, each with a pass through
 // registers after it.  A step of 64 x 64 float takes some 8000 cycles: 1000, 1900 and
 // 1500 in the three products (their latency in it; E E has since lost half its
-// terms) and 1200 to 1300 in each pass.  1024 x 64 x 64 float: 67 us, 512 blocks,
-// three to an SM; its 33.5 MB and 16 GFLOP would take 8.  32 x 128 x 1024 bf16: 67 us
+// terms) and 1200 to 1300 in each pass.  1024 x 64 x 64 float: 66 us, 512 blocks,
+// three to an SM; its 33.5 MB and 16 GFLOP would take 8.  32 x 128 x 1024 bf16: 70 us
 // in clusters of four, 10.5 a step, half of it the exchange of E (two cluster
 // barriers and 64 KB a block); 32 x 128 x 256, without the exchange, 36 us.
 #pragma once

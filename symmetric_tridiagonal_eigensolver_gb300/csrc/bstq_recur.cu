@@ -4,7 +4,8 @@
 // Both directions are one pass over memory.  A tile is 64 channels (a pair to a
 // lane) by W * L tokens (L to each of W = 8 or 11 warps).  Per tile these warps
 //   1. turn r into q_t = 1 - a_t and run their L tokens from a zero state, which
-//      gives each warp's map h -> h + (v - Q h), Q = 1 - exp(-sum of z);
+//      gives each warp's map h -> h + (v - Q h), Q = 1 - exp(-sum of z) (the
+//      gradients: h -> A h + v, in the form of decay());
 //   2. wait for the state that enters their tokens, run them again from it and
 //      leave h in place of x in shared memory;
 // each copies its own rows in and out (TMA, two stages: the next tile's rows
@@ -26,7 +27,9 @@
 //
 // Rounding: a state is updated as h + q (x - h), never as a product with a decay
 // that was rounded near one, and maps carry Q = 1 - A for the same reason: over
-// 32768 tokens a product of float decays drifts by 1e-4, this form by 3e-7.
+// 32768 tokens a product of float decays drifts by 1e-4, this form by 3e-7.  That is
+// relative to x and h; the gradients are products with a, s and 1 - s, which may be
+// small, and keep the digits of those too.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -217,9 +220,9 @@ constexpr uint32_t kUnset = 0xffffffffu;
 
 // Warps of a tile and tokens of a lane: eight warps and three blocks to an SM
 // forward; the gradients, with four tensors and more registers, do better in two
-// blocks of eleven warps (8 x 2048 x 4096 bf16 157 us against 164 with eight in three
-// blocks, 1 x 32768 x 1024 125 against 131, 4 x 4096 x 1024 float 97 against 115; ten
-// and twelve warps lie between).
+// blocks of eleven warps (8 x 2048 x 4096 bf16 175 us against 186 with eight in three
+// blocks, 192 with ten and 184 with twelve in two; 1 x 32768 x 1024 143 against 147,
+// 153 and 142).
 template <typename T, bool GRAD>
 struct Tile {
     static constexpr int W = GRAD ? 11 : 8, BLOCKS = GRAD ? 2 : 3;
