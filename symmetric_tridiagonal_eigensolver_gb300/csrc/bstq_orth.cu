@@ -286,7 +286,7 @@ constexpr int kOutBytes = 4096;  // of each warp that takes sums out: two pieces
 // CTAS == 2: a pair of blocks works on a tile of 256 rows, each with its 128 rows
 // of the left factor and half of the columns of the right one: 32 KB for a block of
 // K that the tensor cores take 512 cycles for, against 48 KB of a 128 x 256 tile
-// (2 x 4096 x 4096 bf16: 2.12 ms without pairs, 1.82 with).
+// (2 x 4096 x 4096 bf16 at burst clocks: 2.12 ms without pairs, 1.82 with).
 template <int BN, int PLANES, int CTAS>
 struct Shape {
     static constexpr int kA = kBM * kBK * 2, kB = BN / CTAS * kBK * 2;
@@ -491,8 +491,9 @@ __device__ __forceinline__ void epilogue32(const ProductArgs &a, const CUtensorM
 // X X^T of 777 x 1531 float took 22 us, by TMA 15.6, and E E 18.4 and 12.1).
 //
 // What bounds it: a block takes 64 bytes a cycle from L2, in which a pair's tile of
-// 256 x 256 just keeps the tensor cores busy; 4096 x 4096 x 2 bf16 runs at 1.5
-// PFLOP/s (78 % of the measured bf16 rate).  With fewer tiles than SMs one tile's way
+// 256 x 256 just keeps the tensor cores busy; 2 x 4096 x 4096 bf16 runs at 1.3
+// PFLOP/s in a stream of passes, where the power limit holds (77 % of the measured
+// sustained rate), and at 1.5 at burst clocks.  With fewer tiles than SMs one tile's way
 // along K is the time, and below 1024 rows the way in and out: some 9 us a product
 // of 512 x 512, of which 1.3 are the first copy's latency, 3.8 the products, 1.4 the
 // sums' way out.  Sharing a tile's K among several blocks, in a cluster or through
